@@ -381,6 +381,144 @@ moe_status moe_router_stats(const moe_config* cfg, const float* s, const float* 
                             float alpha_seq, float* stats, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Around and inside a sublayer x + dropout(MoE(norm(x))).  The pages fix no
+ * norm, no dropout and no block format: these are deployment operators beside
+ * the layer's, with the conventions of the entry points above (host checks
+ * first, nothing enqueued on failure, no allocation, no host synchronisation,
+ * bitwise reproducible).  dtype is MOE_DTYPE_F32 or MOE_DTYPE_BF16; statistics,
+ * gains, scales and their gradients are float32; every sum runs in fp32 and an
+ * output is rounded once.
+ */
+enum {
+  MOE_NORM_LAYER = 0,   /* y = (x - mean) * rstd * gamma + beta, rstd = 1 / sqrt(var + eps)   */
+  MOE_NORM_RMS = 1      /* y = x * rstd * gamma + beta, rstd = 1 / sqrt(mean(x^2) + eps)      */
+};
+
+/*
+ * Norm of the rows in front of the router and the experts.
+ *   x [n_rows, d] (dtype); gamma [d] float32 or NULL for 1; beta [d] float32
+ *   or NULL for 0; eps > 0 (var is the mean of (x - mean)^2 over the d columns).
+ *   out    [n_rows, d] (dtype), or NULL when codes is given.  May be x itself.
+ *   mean, rstd [n_rows] float32 out, or NULL (the backward reads them; mean is
+ *          written as 0 for MOE_NORM_RMS).
+ *   codes  [n_rows, d] e4m3 and scales [n_rows, ceil(d / 128)] float32, or both
+ *          NULL: the output once more as moe_quantize_tiles writes it, bit for
+ *          bit (it quantizes the values as rounded to dtype).  d must then be a
+ *          multiple of 16.
+ * 1 <= d <= 16384 (MOE_ERR_UNSUPPORTED above); n_rows = 0 is allowed.
+ */
+moe_status moe_layer_norm(const void* x, int32_t dtype, int64_t n_rows, int32_t d, int32_t kind,
+                          const float* gamma, const float* beta, float eps, void* out, float* mean,
+                          float* rstd, uint8_t* codes, float* scales, void* stream);
+
+/*
+ * Backward of moe_layer_norm.  With xhat = (x - mean) * rstd (mean = 0 for
+ * MOE_NORM_RMS) and g = gamma * dy:
+ *   dx     = rstd * (g - mean_d(g) - xhat * mean_d(g * xhat)) + dres
+ *            (without mean_d(g) for MOE_NORM_RMS)
+ *   dgamma = sum_rows dy * xhat        dbeta = sum_rows dy
+ *   dy, x [n_rows, d] (dtype); gamma [d] or NULL for 1; mean (NULL allowed for
+ *   MOE_NORM_RMS) and rstd [n_rows] as moe_layer_norm wrote them.
+ *   dres [n_rows, d] (dtype) or NULL: the gradient that reaches x past the norm
+ *   (the residual branch), added before the one rounding.
+ *   dx [n_rows, d] (dtype; may be dy or dres itself); dgamma, dbeta [d] float32
+ *   out, either may be NULL.  n_rows = 0 writes zeros to dgamma and dbeta.
+ *   ws: at least moe_layer_norm_backward_workspace_size bytes, its first 256
+ *   zeroed once (see moe_workspace_size).  The sums over rows run in a fixed
+ *   order; one workspace serves calls whose work does not overlap on the GPU.
+ */
+moe_status moe_layer_norm_backward_workspace_size(int64_t n_rows, int32_t d, size_t* bytes);
+moe_status moe_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_t n_rows,
+                                   int32_t d, int32_t kind, const float* gamma, const float* mean,
+                                   const float* rstd, const void* dres, void* dx, float* dgamma,
+                                   float* dbeta, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Dropout with the residual behind the experts:
+ *   out_i = res_i + (u_i >= p ? x_i / (1 - p) : 0),  i = 0 .. n - 1 (flat),
+ * and its backward  dx_i = (u_i >= p ? dy_i / (1 - p) : 0).
+ * The mask is drawn from a counter and never stored: u_i = word / 2^32 of
+ * Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy
+ * as 1, 2, 3", 2011), word i % 4 of the block with key rng[0] and counter
+ * (i / 4, rng[1]), both as pairs of 32-bit words, low word first.  Forward and
+ * backward with the same rng, p and n draw the same mask.
+ *   rng [2] uint64 on the DEVICE: the generator's seed and the number of this
+ *   draw (8-byte aligned).  It is read when the kernel runs, so a captured graph draws anew
+ *   once the caller changes it; no two draws may share (rng[0], rng[1]).
+ *   x, res, out [n] (dtype); res may be NULL for 0; out may be x or res itself.
+ *   0 <= p <= 1; p = 1 keeps nothing.  Dropped values are not read into the
+ *   result: an infinity or NaN there leaves out_i = res_i.
+ */
+moe_status moe_dropout_add(const void* x, const void* res, int32_t dtype, int64_t n, double p,
+                           const uint64_t* rng, void* out, void* stream);
+moe_status moe_dropout_backward(const void* dy, int32_t dtype, int64_t n, double p,
+                                const uint64_t* rng, void* dx, void* stream);
+
+/*
+ * e4m3 with one float32 scale for each block of 128: rows of activations in
+ * tiles of 1 x 128 (moe_quantize_tiles), weights in blocks of 128 x 128
+ * (moe_quantize_blocks); the last tile or block of a dimension may be partial.
+ * A value is code * scale.  The two quantizers write power-of-two scales by
+ * the rule of moe_quantize_rows (the smallest s >= 2^-126 with
+ * max |x| / s <= 448, 1 for zeros; codes to the nearest, ties to even);
+ * moe_block_matmul and moe_block_ffn take any float32 scales, so weights stored with
+ * scales of another rule (max / 448) need no conversion.  Codes and scales are
+ * separate arrays, as such checkpoints store them.  Values must be finite; a NaN
+ * becomes the code of NaN.
+ *   src [n_rows, cols] or [n_mats, rows, cols] (src_dtype), 16-byte aligned;
+ *   cols a positive multiple of 16; codes 16-byte aligned, same shape as src;
+ *   scales [n_rows, ceil(cols/128)], or [n_mats, ceil(rows/128), ceil(cols/128)].
+ */
+moe_status moe_quantize_tiles(const void* src, int32_t src_dtype, int64_t n_rows, int32_t cols,
+                              uint8_t* codes, float* scales, void* stream);
+moe_status moe_quantize_blocks(const void* src, int32_t src_dtype, int32_t n_mats, int32_t rows,
+                               int32_t cols, uint8_t* codes, float* scales, void* stream);
+
+/*
+ * Grouped matrix product of block-scaled e4m3 operands:
+ *   out[r, j] = row_scale[r] * sum_b x_scale[r, b] * w_scale[g, j / 128, b]
+ *                            * sum_{k in block b} x[r, k] * w[g, j, k]
+ * for offsets[g] <= r < offsets[g + 1]: the products of one block of 128 are
+ * summed by the tensor cores, the scaled blocks in fp32 in ascending order
+ * (a reduction cut into ranges for few rows adds the ranges' sums in order).
+ *   offsets [n_groups + 1] int32 on the device, ascending, offsets[0] >= 0,
+ *   offsets[n_groups] <= max_rows; or NULL with n_groups = 1 for all max_rows rows.
+ *   x [max_rows, k], x_scale [max_rows, ceil(k/128)];  w [n_groups, n_cols, k],
+ *   w_scale [n_groups, ceil(n_cols/128), ceil(k/128)];  row_scale [max_rows] float32
+ *   or NULL for 1.  k a positive multiple of 16; n_cols >= 1; n_groups <= 1024.
+ *   out [max_rows, n_cols], out_dtype MOE_DTYPE_BF16 or MOE_DTYPE_F32.  Rows
+ *   outside [offsets[0], offsets[n_groups]) are left as they were.
+ *   ws: its first 256 bytes zeroed once; offsets out of range set its error
+ *   word (MOE_DEVERR_INDEX) and the group is skipped.
+ */
+moe_status moe_block_matmul_workspace_size(int32_t n_groups, int32_t n_cols, int32_t k,
+                                           int32_t max_rows, size_t* bytes);
+moe_status moe_block_matmul(int32_t n_groups, int32_t n_cols, int32_t k, int32_t max_rows,
+                            const int32_t* offsets, const uint8_t* x, const float* x_scale,
+                            const uint8_t* w, const float* w_scale, const float* row_scale,
+                            int32_t out_dtype, void* out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Grouped SwiGLU experts on block-scaled e4m3 weights, the block-scaled form of
+ * moe_expert_ffn:  out[r] = row_scale[r] * SwiGLU_g(x[r]).  The SwiGLU product
+ * is taken in fp32 and quantized in tiles of 1 x 128 (as moe_quantize_tiles)
+ * before W_down.
+ *   x [max_rows, d_model] codes with x_scale [max_rows, ceil(d_model/128)] (from
+ *   moe_quantize_tiles or moe_layer_norm; permuted with moe_gather_rows);
+ *   w_gate, w_up [n_experts, d_ffn, d_model], w_down [n_experts, d_model, d_ffn]
+ *   codes with s_* their block scales.  d_model, d_ffn positive multiples of 16.
+ *   offsets, row_scale, out, out_dtype, ws as for moe_block_matmul.
+ */
+moe_status moe_block_ffn_workspace_size(int32_t n_experts, int32_t d_model, int32_t d_ffn,
+                                        int32_t max_rows, size_t* bytes);
+moe_status moe_block_ffn(int32_t n_experts, int32_t d_model, int32_t d_ffn, int32_t max_rows,
+                         const int32_t* offsets, const uint8_t* x, const float* x_scale,
+                         const uint8_t* w_gate, const float* s_gate, const uint8_t* w_up,
+                         const float* s_up, const uint8_t* w_down, const float* s_down,
+                         const float* row_scale, int32_t out_dtype, void* out, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/*
  * moe_permute without a workspace, for callers that cannot allocate device
  * memory for one (a caller whose device memory all belongs to its own pool, a
  * caller enqueuing work while another thread captures a CUDA graph, a

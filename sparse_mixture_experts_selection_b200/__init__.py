@@ -24,11 +24,15 @@ __all__ = [
     "moe_router_stats", "moe_router_stats_workspace_size", "ROUTER_STATS", "moe_permute_noalloc",
     "moe_quantized_bytes", "moe_quantize_rows", "DTYPE_BF16_E4M3", "moe_layer_backward", "moe_gather_rows",
     "moe_set_phase_events", "moe_selftest_bounded_wait", "moe_ep_plan", "moe_expert_ffn_tile_rows",
+    "moe_layer_norm", "moe_layer_norm_backward", "moe_layer_norm_backward_workspace_size", "moe_dropout_add",
+    "moe_dropout_backward", "moe_quantize_tiles", "moe_quantize_blocks", "moe_block_matmul",
+    "moe_block_matmul_workspace_size", "moe_block_ffn", "moe_block_ffn_workspace_size", "NORM_LAYER", "NORM_RMS",
     "SCORE_SIGMOID", "SCORE_SOFTMAX", "DTYPE_F32", "DTYPE_BF16",
 ]
 
 SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
 DTYPE_F32, DTYPE_BF16, DTYPE_BF16_E4M3 = 0, 1, 2
+NORM_LAYER, NORM_RMS = 0, 1
 DEVERR_NONE, DEVERR_WAIT_TIMEOUT, DEVERR_INDEX, DEVERR_RANGE = 0, 1, 2, 3
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE",
           4: "MOE_ERR_CUDA", 5: "MOE_ERR_DEVICE"}
@@ -83,6 +87,18 @@ SIGNATURES = {
     "moe_clear_device_error": (ctypes.c_int, [_P, _P]),
     "moe_set_phase_events": (ctypes.c_int, [ctypes.POINTER(ctypes.c_void_p), _I32]),
     "moe_permute_noalloc": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_layer_norm": (ctypes.c_int, [_P, _I32, ctypes.c_int64, _I32, _I32, _P, _P, ctypes.c_float] + [_P] * 6),
+    "moe_layer_norm_backward_workspace_size": (ctypes.c_int, [ctypes.c_int64, _I32, ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_layer_norm_backward": (ctypes.c_int, [_P, _P, _I32, ctypes.c_int64, _I32, _I32] + [_P] * 8
+                                + [ctypes.c_size_t, _P]),
+    "moe_dropout_add": (ctypes.c_int, [_P, _P, _I32, ctypes.c_int64, ctypes.c_double, _P, _P, _P]),
+    "moe_dropout_backward": (ctypes.c_int, [_P, _I32, ctypes.c_int64, ctypes.c_double, _P, _P, _P]),
+    "moe_quantize_tiles": (ctypes.c_int, [_P, _I32, ctypes.c_int64, _I32, _P, _P, _P]),
+    "moe_quantize_blocks": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _P, _P, _P]),
+    "moe_block_matmul_workspace_size": (ctypes.c_int, [_I32] * 4 + [ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_block_matmul": (ctypes.c_int, [_I32] * 4 + [_P] * 6 + [_I32, _P, _P, ctypes.c_size_t, _P]),
+    "moe_block_ffn_workspace_size": (ctypes.c_int, [_I32] * 4 + [ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_block_ffn": (ctypes.c_int, [_I32] * 4 + [_P] * 10 + [_I32, _P, _P, ctypes.c_size_t, _P]),
     "moe_selftest_bounded_wait": (ctypes.c_int, [_P, ctypes.c_int64, _P]),
 }
 
@@ -289,3 +305,179 @@ def moe_selftest_bounded_wait(ws, limit_ns: int = 50_000_000, stream=None) -> No
 
 def moe_clear_device_error(ws, stream=None) -> None:
     _check(lib().moe_clear_device_error(_ptr(ws), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# around and inside a sublayer x + dropout(MoE(norm(x)))
+# ---------------------------------------------------------------------------
+def _tensors(**checks):
+    """The device of a call's tensors (None without any) after a check of them:
+    name=(tensor, dtypes, number of values).  The
+    kernels take dense arrays by pointer, so a strided view, another type, a short
+    tensor or one of another device is refused here.  Plain addresses pass."""
+    device = other = None
+    for name, (t, dtypes, n) in checks.items():
+        if t is None or isinstance(t, int):
+            continue
+        if not t.is_contiguous():
+            raise MoeError(1, f"{name} is not contiguous")
+        if t.element_size() != dtypes[0] or str(t.dtype) not in dtypes:
+            raise MoeError(1, f"{name} has type {t.dtype}, not {' or '.join(map(str, dtypes[1:]))}")
+        if t.numel() < n:
+            raise MoeError(1, f"{name} has {t.numel()} values, {n} are needed")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            other = f"{name} is on {t.device}, another tensor on {device}"
+    if device is not None and device.type != "cuda":
+        other = f"tensors are on {device}, not on a GPU"
+    if other:
+        raise MoeError(1, other)
+    return device
+
+
+class _On:
+    """Make a tensor's device current while a call enqueues its work."""
+
+    def __init__(self, device):
+        import torch
+        self.guard = (torch.cuda.device(device)
+                      if device is not None and device.index != torch.cuda.current_device() else None)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+# the size of a value and the types that are taken
+_F32 = (4, "torch.float32")
+_I32S = (4, "torch.int32")
+_ACT = {DTYPE_F32: _F32, DTYPE_BF16: (2, "torch.bfloat16")}
+_NONE = (0,)                       # an unknown dtype code: no tensor matches
+_CODES = (1, "torch.uint8", "torch.float8_e4m3fn")
+_RNG = (8, "torch.int64", "torch.uint64")
+_BYTES = (1, "torch.uint8")
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def moe_layer_norm(x, dtype: int, n_rows: int, d: int, kind: int, gamma, beta, eps: float, out, mean=None, rstd=None,
+                   codes=None, scales=None, stream=None):
+    """Norm of n_rows rows of d values (NORM_LAYER or NORM_RMS); with codes and
+    scales the output once more in e4m3 tiles of 1 x 128 (see include/moe.h)."""
+    n, act = n_rows * d, _ACT.get(dtype, _NONE)
+    dev = _tensors(x=(x, act, n), gamma=(gamma, _F32, d), beta=(beta, _F32, d), out=(out, act, n),
+                   mean=(mean, _F32, n_rows), rstd=(rstd, _F32, n_rows), codes=(codes, _CODES, n),
+                   scales=(scales, _F32, n_rows * _blocks(d)))
+    with _On(dev):
+        _check(lib().moe_layer_norm(_ptr(x), int(dtype), int(n_rows), int(d), int(kind), _ptr(gamma), _ptr(beta),
+                                    float(eps), _ptr(out), _ptr(mean), _ptr(rstd), _ptr(codes), _ptr(scales),
+                                    _stream(stream)))
+
+
+def moe_layer_norm_backward_workspace_size(n_rows: int, d: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_layer_norm_backward_workspace_size(int(n_rows), int(d), ctypes.byref(n)))
+    return n.value
+
+
+def moe_layer_norm_backward(dy, x, dtype: int, n_rows: int, d: int, kind: int, gamma, mean, rstd, dres, dx, dgamma,
+                            dbeta, ws, stream=None):
+    """Gradients of moe_layer_norm; dres is added to dx (see include/moe.h)."""
+    n, act = n_rows * d, _ACT.get(dtype, _NONE)
+    dev = _tensors(dy=(dy, act, n), x=(x, act, n), gamma=(gamma, _F32, d), mean=(mean, _F32, n_rows),
+                   rstd=(rstd, _F32, n_rows), dres=(dres, act, n), dx=(dx, act, n), dgamma=(dgamma, _F32, d),
+                   dbeta=(dbeta, _F32, d), ws=(ws, _BYTES, 0))
+    with _On(dev):
+        _check(lib().moe_layer_norm_backward(
+            _ptr(dy), _ptr(x), int(dtype), int(n_rows), int(d), int(kind), _ptr(gamma), _ptr(mean), _ptr(rstd),
+            _ptr(dres), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_dropout_add(x, res, dtype: int, n: int, p: float, rng, out, stream=None):
+    """out = res + dropout(x) over n values; rng: int64 [2] on the device, the
+    seed and the number of this draw (see include/moe.h)."""
+    act = _ACT.get(dtype, _NONE)
+    dev = _tensors(x=(x, act, n), res=(res, act, n), rng=(rng, _RNG, 2), out=(out, act, n))
+    with _On(dev):
+        _check(lib().moe_dropout_add(_ptr(x), _ptr(res), int(dtype), int(n), float(p), _ptr(rng), _ptr(out),
+                                     _stream(stream)))
+
+
+def moe_dropout_backward(dy, dtype: int, n: int, p: float, rng, dx, stream=None):
+    """dx = dy through the mask that moe_dropout_add drew with the same rng, p and n."""
+    act = _ACT.get(dtype, _NONE)
+    dev = _tensors(dy=(dy, act, n), rng=(rng, _RNG, 2), dx=(dx, act, n))
+    with _On(dev):
+        _check(lib().moe_dropout_backward(_ptr(dy), int(dtype), int(n), float(p), _ptr(rng), _ptr(dx),
+                                          _stream(stream)))
+
+
+def moe_quantize_tiles(src, src_dtype: int, n_rows: int, cols: int, codes, scales, stream=None):
+    """e4m3 codes and one power-of-two scale for each 1 x 128 tile of the rows."""
+    dev = _tensors(src=(src, _ACT.get(src_dtype, _NONE), n_rows * cols), codes=(codes, _CODES, n_rows * cols),
+                   scales=(scales, _F32, n_rows * _blocks(cols)))
+    with _On(dev):
+        _check(lib().moe_quantize_tiles(_ptr(src), int(src_dtype), int(n_rows), int(cols), _ptr(codes), _ptr(scales),
+                                        _stream(stream)))
+
+
+def moe_quantize_blocks(src, src_dtype: int, n_mats: int, rows: int, cols: int, codes, scales, stream=None):
+    """e4m3 codes and one power-of-two scale for each 128 x 128 block of the matrices."""
+    n = n_mats * rows * cols
+    dev = _tensors(src=(src, _ACT.get(src_dtype, _NONE), n), codes=(codes, _CODES, n),
+                   scales=(scales, _F32, n_mats * _blocks(rows) * _blocks(cols)))
+    with _On(dev):
+        _check(lib().moe_quantize_blocks(_ptr(src), int(src_dtype), int(n_mats), int(rows), int(cols), _ptr(codes),
+                                         _ptr(scales), _stream(stream)))
+
+
+def moe_block_matmul_workspace_size(n_groups: int, n_cols: int, k: int, max_rows: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_block_matmul_workspace_size(int(n_groups), int(n_cols), int(k), int(max_rows), ctypes.byref(n)))
+    return n.value
+
+
+def moe_block_matmul(n_groups: int, n_cols: int, k: int, max_rows: int, offsets, x, x_scale, w, w_scale, row_scale,
+                     out_dtype: int, out, ws, stream=None):
+    """Grouped product of block-scaled e4m3 operands (see include/moe.h); offsets
+    None with one group takes all max_rows rows."""
+    dev = _tensors(offsets=(offsets, _I32S, n_groups + 1), x=(x, _CODES, max_rows * k),
+                   x_scale=(x_scale, _F32, max_rows * _blocks(k)), w=(w, _CODES, n_groups * n_cols * k),
+                   w_scale=(w_scale, _F32, n_groups * _blocks(n_cols) * _blocks(k)),
+                   row_scale=(row_scale, _F32, max_rows), out=(out, _ACT.get(out_dtype, _NONE), max_rows * n_cols),
+                   ws=(ws, _BYTES, 0))
+    with _On(dev):
+        _check(lib().moe_block_matmul(int(n_groups), int(n_cols), int(k), int(max_rows), _ptr(offsets), _ptr(x),
+                                      _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(row_scale), int(out_dtype),
+                                      _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_block_ffn_workspace_size(n_experts: int, d_model: int, d_ffn: int, max_rows: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_block_ffn_workspace_size(int(n_experts), int(d_model), int(d_ffn), int(max_rows),
+                                              ctypes.byref(n)))
+    return n.value
+
+
+def moe_block_ffn(n_experts: int, d_model: int, d_ffn: int, max_rows: int, offsets, x, x_scale, w_gate, s_gate, w_up,
+                  s_up, w_down, s_down, row_scale, out_dtype: int, out, ws, stream=None):
+    """Grouped SwiGLU experts on block-scaled e4m3 weights (see include/moe.h)."""
+    n = n_experts * d_model * d_ffn
+    nb = n_experts * _blocks(d_model) * _blocks(d_ffn)
+    dev = _tensors(offsets=(offsets, _I32S, n_experts + 1), x=(x, _CODES, max_rows * d_model),
+                   x_scale=(x_scale, _F32, max_rows * _blocks(d_model)), w_gate=(w_gate, _CODES, n),
+                   s_gate=(s_gate, _F32, nb), w_up=(w_up, _CODES, n), s_up=(s_up, _F32, nb),
+                   w_down=(w_down, _CODES, n), s_down=(s_down, _F32, nb), row_scale=(row_scale, _F32, max_rows),
+                   out=(out, _ACT.get(out_dtype, _NONE), max_rows * d_model), ws=(ws, _BYTES, 0))
+    with _On(dev):
+        _check(lib().moe_block_ffn(int(n_experts), int(d_model), int(d_ffn), int(max_rows), _ptr(offsets), _ptr(x),
+                                   _ptr(x_scale), _ptr(w_gate), _ptr(s_gate), _ptr(w_up), _ptr(s_up), _ptr(w_down),
+                                   _ptr(s_down), _ptr(row_scale), int(out_dtype), _ptr(out), _ptr(ws), ws.numel(),
+                                   _stream(stream)))

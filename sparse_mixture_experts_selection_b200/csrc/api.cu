@@ -6,12 +6,13 @@
 #include <cstdio>
 #include <cstring>
 
+#include "api.h"
 #include "common.cuh"
 #include "kernels.h"
 
-namespace {
+static thread_local char g_detail[512] = "";
 
-thread_local char g_detail[512] = "";
+namespace moe {
 
 moe_status fail(moe_status s, const char* fmt, ...) {
   va_list ap;
@@ -21,16 +22,38 @@ moe_status fail(moe_status s, const char* fmt, ...) {
   return s;
 }
 
-constexpr int kChunkShift = 8;          // histogram chunk = 256 tokens (the scatter block)
-constexpr size_t kAlign = 256;
+moe_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
+  if (!ws) return fail(MOE_ERR_WORKSPACE, "ws is NULL");
+  if (reinterpret_cast<uintptr_t>(ws) % kAlign) return fail(MOE_ERR_WORKSPACE, "ws is not 256-byte aligned");
+  if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "ws_bytes=%zu < required %zu", ws_bytes, need);
+  return MOE_OK;
+}
 
-size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
+moe_status cuda_status() {
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "CUDA error: %s", cudaGetErrorString(e));
+  return MOE_OK;
+}
+
+}  // namespace moe
+
+namespace {
+
+using moe::aligned16;
+using moe::align_up;
+using moe::at;
+using moe::check_ws;
+using moe::cuda_status;
+using moe::fail;
+using moe::kAlign;
+
+constexpr int kChunkShift = 8;          // histogram chunk = 256 tokens (the scatter block)
+
 // bytes of an activation element (h, y, x_perm, A, slots): 2 for the bf16 and
 // e4m3-weight layers (bf16; a layer's own slot rows fp16), 4 for fp32 layers
 size_t elem_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
 int act_dtype(int dtype) { return dtype == MOE_DTYPE_F32 ? MOE_DTYPE_F32 : MOE_DTYPE_BF16; }
 bool is_q8(int dtype) { return dtype == MOE_DTYPE_BF16_E4M3; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int64_t capacity_rows(const moe_config& c) {
   const int64_t tk = (int64_t)c.T * c.K;
@@ -162,30 +185,6 @@ moe_status validate(const moe_config* cfg) {
   if (c.train && (c.d_model % 64 || c.d_ffn % 64 || (c.E_s > 0 && c.d_ffn_shared % 64)))
     return fail(MOE_ERR_UNSUPPORTED, "train needs d_model, d_ffn, d_ffn_shared multiples of 64");
   return MOE_OK;
-}
-
-moe_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
-  if (!ws) return fail(MOE_ERR_WORKSPACE, "ws is NULL");
-  if (reinterpret_cast<uintptr_t>(ws) % kAlign) return fail(MOE_ERR_WORKSPACE, "ws is not 256-byte aligned");
-  if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "ws_bytes=%zu < required %zu", ws_bytes, need);
-  return MOE_OK;
-}
-
-moe_status cuda_status() {
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "CUDA error: %s", cudaGetErrorString(e));
-  return MOE_OK;
-}
-
-#define MOE_CHECK(x) do { moe_status s_ = (x); if (s_ != MOE_OK) return s_; } while (0)
-#define MOE_NONNULL(p) do { if (!(p)) return fail(MOE_ERR_INVALID_ARG, #p " is NULL"); \
-    if (!aligned16(p)) return fail(MOE_ERR_INVALID_ARG, #p " is not 16-byte aligned"); } while (0)
-#define MOE_ALIGNED(p) do { if ((p) && !aligned16(p)) return fail(MOE_ERR_INVALID_ARG, #p " is not 16-byte aligned"); } while (0)
-#define MOE_ALIGNED4(p) do { if ((p) && (reinterpret_cast<uintptr_t>(p) & 3u)) return fail(MOE_ERR_INVALID_ARG, #p " is not 4-byte aligned"); } while (0)
-#define MOE_NONNULL4(p) do { if (!(p)) return fail(MOE_ERR_INVALID_ARG, #p " is NULL"); MOE_ALIGNED4(p); } while (0)
-
-template <typename T> T* at(void* ws, size_t off) {
-  return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
 }
 
 bool use_tensor_cores(int dtype) { return dtype != MOE_DTYPE_F32; }

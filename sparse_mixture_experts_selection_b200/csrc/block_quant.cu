@@ -1,0 +1,162 @@
+// e4m3 codes with one power-of-two scale for each 1 x 128 tile of a row
+// (activations) or each 128 x 128 block of a matrix (weights): the smallest s
+// with max |x| / s <= 448, each x / s rounded to the nearest code.  Dividing by
+// a power of two is exact, so the codes depend on the values alone.
+#include "api.h"
+#include "common.cuh"
+#include "e4m3.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+// Eight values from 16-byte loads.
+__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
+  const uint4 q = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+__device__ __forceinline__ float top8(const float (&v)[8]) {
+  float t = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t = fmaxf(t, fabsf(v[i]));
+  return t;
+}
+
+__device__ __forceinline__ void store8(uint8_t* p, const float (&v)[8], float inv) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(e4m3_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                                            e4m3_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+}
+
+// Half a warp per tile, eight values per lane: one 16-byte load (bf16) and one
+// 8-byte store of codes a lane, no shared memory.  Bound by memory.
+template <typename TIn>
+__global__ void __launch_bounds__(256) quantize_tiles_kernel(const TIn* __restrict__ src, int64_t n_tiles, int tiles,
+                                                             int cols, uint8_t* __restrict__ codes,
+                                                             float* __restrict__ scales) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x % 16;
+  // whole warps walk together: their shuffles name all lanes
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x / 16);
+  for (int64_t t0 = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) / 32 * 2; t0 < n_tiles; t0 += step) {
+    const int64_t t = t0 + threadIdx.x / 16 % 2;
+    const int64_t r = t / tiles;
+    const int c = (int)(t - r * tiles) * 128 + lane * 8;
+    const bool valid = t < n_tiles && c < cols;
+    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (valid) load8(src + r * cols + c, v);
+    float top = top8(v);
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+    const int e = e4m3_scale_exponent(top);
+    if (valid) {
+      store8(codes + r * cols + c, v, pow2(-e));
+      if (lane == 0) scales[t] = pow2(e);
+    }
+  }
+}
+
+// A block of 256 threads per 128 x 128 block: 16 threads across a row, eight
+// rows each, all values in registers between the maximum and the codes.
+template <typename TIn>
+__global__ void __launch_bounds__(256) quantize_blocks_kernel(const TIn* __restrict__ src, int rows, int cols,
+                                                              int row_blocks, int col_blocks,
+                                                              uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  __shared__ float tops[8];
+  const int64_t b = blockIdx.x;
+  const int cb = (int)(b % col_blocks);
+  const int rb = (int)(b / col_blocks % row_blocks);
+  const int64_t m = b / col_blocks / row_blocks;
+  const int c = cb * 128 + threadIdx.x % 16 * 8;
+  const int64_t base = m * rows * cols + c;
+  float v[8][8];
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = rb * 128 + threadIdx.x / 16 + 16 * i;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    if (r < rows && c < cols) load8(src + base + (int64_t)r * cols, v[i]);
+    top = fmaxf(top, top8(v[i]));
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+  if (threadIdx.x % kWarp == 0) tops[threadIdx.x / kWarp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) top = fmaxf(top, tops[w]);
+  const int e = e4m3_scale_exponent(top);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = rb * 128 + threadIdx.x / 16 + 16 * i;
+    if (r < rows && c < cols) store8(codes + base + (int64_t)r * cols, v[i], pow2(-e));
+  }
+  if (threadIdx.x == 0) scales[b] = pow2(e);
+}
+
+moe_status check_source(const void* src, int dtype, int cols, const void* codes, const void* scales, bool empty) {
+  if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16) return fail(MOE_ERR_INVALID_ARG, "src_dtype=%d", dtype);
+  if (cols < 16 || cols % 16) return fail(MOE_ERR_INVALID_ARG, "cols=%d must be a positive multiple of 16", cols);
+  if (empty) return MOE_OK;
+  MOE_NONNULL(src); MOE_NONNULL(codes); MOE_NONNULL4(scales);
+  return MOE_OK;
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_tiles(const void* src, int src_dtype, int64_t n_rows, int cols, uint8_t* codes,
+                                  float* scales, cudaStream_t st) {
+  const int tiles = (cols + 127) / 128;
+  const int64_t n_tiles = n_rows * tiles;
+  const int64_t want = (n_tiles + 15) / 16;
+  const dim3 grid((unsigned)(want < 148 * 8 ? want : 148 * 8));
+  if (src_dtype == MOE_DTYPE_BF16)
+    return launch_pdl(quantize_tiles_kernel<uint16_t>, grid, dim3(256), 0, st, static_cast<const uint16_t*>(src),
+                      n_tiles, tiles, cols, codes, scales);
+  return launch_pdl(quantize_tiles_kernel<float>, grid, dim3(256), 0, st, static_cast<const float*>(src), n_tiles,
+                    tiles, cols, codes, scales);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_quantize_tiles(const void* src, int32_t src_dtype, int64_t n_rows, int32_t cols,
+                                         uint8_t* codes, float* scales, void* stream) {
+  if (n_rows < 0) return fail(MOE_ERR_INVALID_ARG, "n_rows=%lld < 0", (long long)n_rows);
+  MOE_CHECK(check_source(src, src_dtype, cols, codes, scales, n_rows == 0));
+  if (n_rows == 0) return MOE_OK;
+  const cudaError_t e = launch_quantize_tiles(src, src_dtype, n_rows, cols, codes, scales,
+                                              static_cast<cudaStream_t>(stream));
+  return e != cudaSuccess ? fail(MOE_ERR_CUDA, "quantize launch: %s", cudaGetErrorString(e)) : MOE_OK;
+}
+
+extern "C" moe_status moe_quantize_blocks(const void* src, int32_t src_dtype, int32_t n_mats, int32_t rows,
+                                          int32_t cols, uint8_t* codes, float* scales, void* stream) {
+  if (n_mats < 0 || rows < 0) return fail(MOE_ERR_INVALID_ARG, "n_mats=%d rows=%d", n_mats, rows);
+  const bool empty = n_mats == 0 || rows == 0;
+  MOE_CHECK(check_source(src, src_dtype, cols, codes, scales, empty));
+  if (empty) return MOE_OK;
+  const int rb = (rows + 127) / 128, cb = (cols + 127) / 128;
+  const int64_t n = (int64_t)n_mats * rb * cb;
+  if (n > 0x7FFFFFFF) return fail(MOE_ERR_UNSUPPORTED, "%lld blocks", (long long)n);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (src_dtype == MOE_DTYPE_BF16)
+    quantize_blocks_kernel<uint16_t><<<(unsigned)n, 256, 0, st>>>(static_cast<const uint16_t*>(src), rows, cols, rb,
+                                                                  cb, codes, scales);
+  else
+    quantize_blocks_kernel<float><<<(unsigned)n, 256, 0, st>>>(static_cast<const float*>(src), rows, cols, rb, cb,
+                                                               codes, scales);
+  return cuda_status();
+}

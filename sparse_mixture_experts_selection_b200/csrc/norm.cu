@@ -1,0 +1,499 @@
+// Norm of the rows in front of the router and the experts, and its backward.
+//
+//   c = x - mean(x) (layer) or x (rms);  rstd = 1 / sqrt(mean(c^2) + eps)
+//   y = c * rstd * gamma + beta;  optionally y once more as e4m3 tiles of 1 x 128
+//   backward, xhat = c * rstd, g = gamma * dy:
+//     dx = rstd * (g - mean(g) [layer] - xhat * mean(g * xhat)) + dres
+//     dgamma = sum_rows dy * xhat,  dbeta = sum_rows dy
+//
+// Both are bound by memory: one pass over the data.  A row lives in the registers of W warps
+// (NV 16-byte vectors per lane), so the centred sum of squares needs no second
+// read and does not cancel for rows with a large mean; sums go lane -> warp
+// (shuffles) -> row (shared memory), always in the same order.
+#include <cmath>
+
+#include "api.h"
+#include "common.cuh"
+#include "e4m3.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxNormCols = 16384;
+constexpr int kNormGrid = 2 * 148;       // blocks of the backward: their partial sums are the workspace
+
+// How rows map to warps: W warps per row, NV vectors of V elements per lane,
+// `slots` rows at a time in a block of `threads`.
+struct NormShape {
+  int W, NV, threads, slots;
+};
+
+NormShape norm_shape(int d, int dtype, int max_nv) {
+  const int V = dtype == MOE_DTYPE_F32 ? 4 : 8;
+  const int nvec = (d + V - 1) / V;
+  NormShape s{};
+  s.W = 1;
+  while (s.W < 32 && (nvec + 32 * s.W - 1) / (32 * s.W) > max_nv) s.W *= 2;
+  const int nv = (nvec + 32 * s.W - 1) / (32 * s.W);
+  s.NV = nv <= 1 ? 1 : nv <= 2 ? 2 : 4;
+  s.threads = s.W <= 8 ? 256 : 32 * s.W;
+  s.slots = s.threads / (32 * s.W);
+  return s;
+}
+
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+  static constexpr int N = 4;
+  __device__ static void unpack(const uint4& q, float (&v)[4]) {
+    v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y);
+    v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
+  }
+  __device__ static uint4 pack(const float (&v)[4]) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+  __device__ static uint32_t bits(float v) { return __float_as_uint(v); }
+  __device__ static float value(uint32_t b) { return __uint_as_float(b); }
+};
+template <> struct Vec<bf16> {
+  static constexpr int N = 8;
+  __device__ static void unpack(const uint4& q, float (&v)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  __device__ static uint4 pack(const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// One lane's share of a row.  VECTOR: slot i of the lane is the 16-byte vector
+// i * 32W + lane, when d is a whole number of vectors (every row then starts
+// on 16 bytes); otherwise element j of slot i is column (i * N + j) * 32W + lane,
+// single loads that neighbouring lanes make side by side.
+template <typename T, int W, bool VECTOR>
+struct Row {
+  static constexpr int N = Vec<T>::N, L = 32 * W;
+  __device__ static int col(int i, int j, int lane) { return VECTOR ? (i * L + lane) * N + j : (i * N + j) * L + lane; }
+  // columns at or beyond d read as `other`
+  __device__ static void load(const T* p, int d, int i, int lane, float other, float (&v)[N]) {
+    if (VECTOR) {
+      const int c = (i * L + lane) * N;
+      if (c < d) {
+        Vec<T>::unpack(*reinterpret_cast<const uint4*>(p + c), v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = other;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int c = col(i, j, lane);
+        v[j] = c < d ? to_f32<T>(p[c]) : other;
+      }
+    }
+  }
+  __device__ static void store(T* p, int d, int i, int lane, const float (&v)[N]) {
+    if (VECTOR) {
+      const int c = (i * L + lane) * N;
+      if (c < d) *reinterpret_cast<uint4*>(p + c) = Vec<T>::pack(v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int c = col(i, j, lane);
+        if (c < d) p[c] = from_f32<T>(v[j]);
+      }
+    }
+  }
+  // the same columns of an fp32 array (null: `other`)
+  __device__ static void load_f32(const float* p, int d, int i, int lane, float other, float (&v)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = other;
+    if (!p) return;
+    if (VECTOR) {
+      const int c = (i * L + lane) * N;
+      if (c >= d) return;
+      if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) {       // gains are only promised 4-byte alignment
+#pragma unroll
+        for (int j = 0; j < N; j += 4) {
+          const float4 q = *reinterpret_cast<const float4*>(p + c + j);
+          v[j] = q.x; v[j + 1] = q.y; v[j + 2] = q.z; v[j + 3] = q.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = p[c + j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int c = col(i, j, lane);
+        if (c < d) v[j] = p[c];
+      }
+    }
+  }
+};
+
+// Sums of K values over the W warps of a row, the same in every lane.  Called by
+// all threads of the block; buf holds two generations so that one barrier per
+// call is enough.
+template <int W, int K>
+__device__ __forceinline__ void row_sum(float (&v)[K], float (*buf)[32 * K], int& gen) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(kFull, v[k], off);
+  if (W == 1) return;
+  const int warp = threadIdx.x / kWarp;
+  float* b = buf[gen];
+  if (threadIdx.x % kWarp == 0)
+#pragma unroll
+    for (int k = 0; k < K; ++k) b[k * 32 + warp] = v[k];
+  __syncthreads();
+  const int w0 = warp / W * W;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) s += b[k * 32 + w0 + w];
+    v[k] = s;
+  }
+  gen ^= 1;
+}
+
+struct NormArgs {
+  const void* x;
+  const float *gamma, *beta;
+  void* out;
+  float *mean, *rstd;
+  uint8_t* codes;
+  float* scales;
+  int64_t n_rows;
+  int d;
+  float eps;
+};
+
+template <typename T, int W, int NV, bool VECTOR, bool LAYER, bool TILES>
+__global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W) norm_kernel(const NormArgs a) {
+  using R = Row<T, W, VECTOR>;
+  constexpr int N = R::N, L = R::L, SLOTS = (W <= 8 ? 256 : 32 * W) / L;
+  __shared__ float buf[2][32];
+  int gen = 0;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x % L;
+  const int64_t r = (int64_t)blockIdx.x * SLOTS + threadIdx.x / L;
+  const bool valid = r < a.n_rows;
+  const int d = a.d;
+  const T* x = static_cast<const T*>(a.x) + (valid ? r : 0) * d;
+  float v[NV][N];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) R::load(x, d, i, lane, 0.0f, v[i]);
+  const float inv_d = 1.0f / (float)d;
+  float mean = 0.0f;
+  if (LAYER) {
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) s[0] += v[i][j];
+    row_sum<W, 1>(s, buf, gen);
+    mean = s[0] * inv_d;
+  }
+  float q[1] = {0.0f};
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (LAYER) v[i][j] = R::col(i, j, lane) < d ? v[i][j] - mean : 0.0f;
+      q[0] = fmaf(v[i][j], v[i][j], q[0]);
+    }
+  row_sum<W, 1>(q, buf, gen);
+  const float rstd = 1.0f / sqrtf(q[0] * inv_d + a.eps);
+  if (valid && lane == 0) {
+    if (a.mean) a.mean[r] = mean;
+    if (a.rstd) a.rstd[r] = rstd;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float g[N], b[N];
+    R::load_f32(a.gamma, d, i, lane, 1.0f, g);
+    R::load_f32(a.beta, d, i, lane, 0.0f, b);
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[i][j] = fmaf(v[i][j] * rstd, g[j], b[j]);
+    if (valid && a.out) R::store(static_cast<T*>(a.out) + r * d, d, i, lane, v[i]);
+    if (TILES) {
+      // the stored values, in tiles of 128 columns = 128 / N neighbouring lanes
+      const int c = (i * L + lane) * N;
+      float top = 0.0f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        v[i][j] = c < d ? to_f32<T>(from_f32<T>(v[i][j])) : 0.0f;
+        top = fmaxf(top, fabsf(v[i][j]));
+      }
+#pragma unroll
+      for (int off = 64 / N; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+      const int e = e4m3_scale_exponent(top);
+      const float inv = pow2(-e);
+      if (valid && c < d) {
+        uint32_t w[N / 4];
+#pragma unroll
+        for (int j = 0; j < N; j += 4)
+          w[j / 4] = e4m3_pack4(v[i][j] * inv, v[i][j + 1] * inv, v[i][j + 2] * inv, v[i][j + 3] * inv);
+        uint8_t* out = a.codes + r * d + c;
+        if (N == 8) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[N / 4 - 1]);
+        else *reinterpret_cast<uint32_t*>(out) = w[0];
+        if (c % 128 == 0) a.scales[r * ((d + 127) / 128) + c / 128] = pow2(e);
+      }
+    }
+  }
+}
+
+struct NormGradArgs {
+  const void *dy, *x, *dres;
+  const float *gamma, *mean, *rstd;
+  void* dx;
+  float* part;               // [parts][2][d]: dgamma, dbeta of one block slot's rows
+  int64_t n_rows;
+  int d, want_sums;
+};
+
+// A block walks rows blockIdx * SLOTS + slot, += grid * SLOTS; its lanes keep
+// their columns' gains and the running dgamma, dbeta in registers.
+template <typename T, int W, int NV, bool VECTOR, bool LAYER>
+__global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W) norm_grad_kernel(const NormGradArgs a) {
+  using R = Row<T, W, VECTOR>;
+  constexpr int N = R::N, L = R::L, SLOTS = (W <= 8 ? 256 : 32 * W) / L;
+  __shared__ float buf[2][64];
+  int gen = 0;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x % L, slot = threadIdx.x / L;
+  const int d = a.d;
+  const float inv_d = 1.0f / (float)d;
+  float gamma[NV][N], dg[NV][N], db[NV][N];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    R::load_f32(a.gamma, d, i, lane, 1.0f, gamma[i]);
+#pragma unroll
+    for (int j = 0; j < N; ++j) dg[i][j] = db[i][j] = 0.0f;
+  }
+  const int64_t step = (int64_t)gridDim.x * SLOTS;
+  for (int64_t r0 = (int64_t)blockIdx.x * SLOTS; r0 < a.n_rows; r0 += step) {
+    const int64_t r = r0 + slot;
+    const bool valid = r < a.n_rows;
+    const T* xr = static_cast<const T*>(a.x) + (valid ? r : r0) * d;
+    const T* dyr = static_cast<const T*>(a.dy) + (valid ? r : r0) * d;
+    float xh[NV][N], dy[NV][N];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      R::load(xr, d, i, lane, 0.0f, xh[i]);
+      R::load(dyr, d, i, lane, 0.0f, dy[i]);
+    }
+    const float rstd = valid ? a.rstd[r] : 0.0f;
+    const float mean = LAYER && valid ? a.mean[r] : 0.0f;
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        if (R::col(i, j, lane) >= d) { xh[i][j] = 0.0f; continue; }
+        xh[i][j] = (xh[i][j] - mean) * rstd;
+        if (valid) {
+          dg[i][j] = fmaf(dy[i][j], xh[i][j], dg[i][j]);
+          db[i][j] += dy[i][j];
+        }
+        dy[i][j] *= gamma[i][j];
+        s[0] += dy[i][j];
+        s[1] = fmaf(dy[i][j], xh[i][j], s[1]);
+      }
+    row_sum<W, 2>(s, buf, gen);
+    const float m1 = LAYER ? s[0] * inv_d : 0.0f, m2 = s[1] * inv_d;
+    if (!valid) continue;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float o[N], res[N];
+      if (a.dres) R::load(static_cast<const T*>(a.dres) + r * d, d, i, lane, 0.0f, res);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        o[j] = rstd * (dy[i][j] - m1 - xh[i][j] * m2);
+        if (a.dres) o[j] += res[j];
+      }
+      R::store(static_cast<T*>(a.dx) + r * d, d, i, lane, o);
+    }
+  }
+  if (!a.want_sums) return;
+  float* part = a.part + ((size_t)blockIdx.x * SLOTS + slot) * 2 * d;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int c = R::col(i, j, lane);
+      if (c < d) { part[c] = dg[i][j]; part[d + c] = db[i][j]; }
+    }
+}
+
+// dgamma (blockIdx.y = 0) and dbeta (1): the parts summed in a fixed order, 32
+// columns per block, eight interleaved runs of parts joined at the end.
+__global__ void __launch_bounds__(256) norm_grad_sum_kernel(const float* part, int parts, int d,
+                                                            float* dgamma, float* dbeta) {
+  __shared__ float s[8][33];
+  pdl_wait();
+  pdl_trigger();
+  float* out = blockIdx.y == 0 ? dgamma : dbeta;
+  if (!out) return;
+  const int cx = threadIdx.x % 32, py = threadIdx.x / 32;
+  const int c = blockIdx.x * 32 + cx;
+  float v = 0.0f;
+  if (c < d)
+    for (int p = py; p < parts; p += 8) v += part[((size_t)p * 2 + blockIdx.y) * d + c];
+  s[py][cx] = v;
+  __syncthreads();
+  if (py == 0 && c < d) {
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t += s[k][cx];
+    out[c] = t;
+  }
+}
+
+template <typename T, int W, int NV, bool VECTOR, bool LAYER>
+cudaError_t start_norm(const NormArgs& a, const NormShape& s, cudaStream_t st) {
+  const dim3 grid((unsigned)((a.n_rows + s.slots - 1) / s.slots));
+  if constexpr (VECTOR) {
+    if (a.codes) return launch_pdl(norm_kernel<T, W, NV, VECTOR, LAYER, true>, grid, dim3(s.threads), 0, st, a);
+  }
+  return launch_pdl(norm_kernel<T, W, NV, VECTOR, LAYER, false>, grid, dim3(s.threads), 0, st, a);
+}
+
+template <typename T, int W, int NV, bool VECTOR, bool LAYER>
+cudaError_t start_norm_grad(const NormGradArgs& a, const NormShape& s, int grid, cudaStream_t st) {
+  return launch_pdl(norm_grad_kernel<T, W, NV, VECTOR, LAYER>, dim3(grid), dim3(s.threads), 0, st, a);
+}
+
+// F(T, W, NV, VECTOR, LAYER) for the shape; one- and two-vector rows take one warp.
+#define MOE_NORM_PICK(F, T, ...)                                                        \
+  [&]() -> cudaError_t {                                                                \
+    auto pick = [&](auto vec, auto layer) -> cudaError_t {                              \
+      constexpr bool VEC = decltype(vec)::value, LAY = decltype(layer)::value;          \
+      if (s.W == 1) {                                                                   \
+        if (s.NV == 1) return F<T, 1, 1, VEC, LAY>(__VA_ARGS__);                        \
+        if (s.NV == 2) return F<T, 1, 2, VEC, LAY>(__VA_ARGS__);                        \
+        return F<T, 1, 4, VEC, LAY>(__VA_ARGS__);                                       \
+      }                                                                                 \
+      MOE_NORM_WIDE(F, T, __VA_ARGS__)                                                  \
+      return cudaErrorInvalidValue;                                                     \
+    };                                                                                  \
+    if (vector) return layer ? pick(std::true_type{}, std::true_type{}) : pick(std::true_type{}, std::false_type{});     \
+    return layer ? pick(std::false_type{}, std::true_type{}) : pick(std::false_type{}, std::false_type{});               \
+  }()
+
+moe_status check_rows(int dtype, int64_t n_rows, int d, int kind) {
+  if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16) return fail(MOE_ERR_INVALID_ARG, "dtype=%d", dtype);
+  if (n_rows < 0) return fail(MOE_ERR_INVALID_ARG, "n_rows=%lld < 0", (long long)n_rows);
+  if (n_rows > (int64_t)1 << 31) return fail(MOE_ERR_UNSUPPORTED, "n_rows=%lld > 2^31", (long long)n_rows);
+  if (d < 1) return fail(MOE_ERR_INVALID_ARG, "d=%d < 1", d);
+  if (d > kMaxNormCols) return fail(MOE_ERR_UNSUPPORTED, "d=%d > %d", d, kMaxNormCols);
+  if (kind != MOE_NORM_LAYER && kind != MOE_NORM_RMS) return fail(MOE_ERR_INVALID_ARG, "kind=%d", kind);
+  return MOE_OK;
+}
+
+constexpr int kNormVecs = 4, kNormGradVecs = 2;
+
+int norm_grad_grid(const NormShape& s, int64_t n_rows) {
+  const int64_t blocks = (n_rows + s.slots - 1) / s.slots;
+  return (int)(blocks < kNormGrid ? blocks : kNormGrid);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+#define MOE_NORM_WIDE(F, T, ...)                                     \
+  if (s.W == 2) return F<T, 2, 4, VEC, LAY>(__VA_ARGS__);            \
+  if (s.W == 4) return F<T, 4, 4, VEC, LAY>(__VA_ARGS__);            \
+  if (s.W == 8) return F<T, 8, 4, VEC, LAY>(__VA_ARGS__);            \
+  if (s.W == 16) return F<T, 16, 4, VEC, LAY>(__VA_ARGS__);          \
+  if (s.W == 32) return F<T, 32, 4, VEC, LAY>(__VA_ARGS__);
+
+extern "C" moe_status moe_layer_norm(const void* x, int32_t dtype, int64_t n_rows, int32_t d, int32_t kind,
+                                     const float* gamma, const float* beta, float eps, void* out, float* mean,
+                                     float* rstd, uint8_t* codes, float* scales, void* stream) {
+  MOE_CHECK(check_rows(dtype, n_rows, d, kind));
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return fail(MOE_ERR_INVALID_ARG, "eps must be positive and finite");
+  if (codes && d % 16) return fail(MOE_ERR_INVALID_ARG, "codes need d=%d to be a multiple of 16", d);
+  if (n_rows == 0) return MOE_OK;          // empty arrays have no addresses
+  if (!out && !codes) return fail(MOE_ERR_INVALID_ARG, "out and codes are both NULL");
+  if (!codes != !scales) return fail(MOE_ERR_INVALID_ARG, "codes and scales go together");
+  MOE_NONNULL(x); MOE_ALIGNED(out); MOE_ALIGNED(codes);
+  MOE_ALIGNED4(gamma); MOE_ALIGNED4(beta); MOE_ALIGNED4(mean); MOE_ALIGNED4(rstd); MOE_ALIGNED4(scales);
+  const NormShape s = norm_shape(d, dtype, kNormVecs);
+  NormArgs a{x, gamma, beta, out, mean, rstd, codes, scales, n_rows, d, eps};
+  const bool layer = kind == MOE_NORM_LAYER;
+  const bool vector = d % (dtype == MOE_DTYPE_F32 ? 4 : 8) == 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == MOE_DTYPE_F32 ? MOE_NORM_PICK(start_norm, float, a, s, st)
+                                               : MOE_NORM_PICK(start_norm, bf16, a, s, st);
+  return e != cudaSuccess ? fail(MOE_ERR_CUDA, "norm launch: %s", cudaGetErrorString(e)) : MOE_OK;
+}
+
+extern "C" moe_status moe_layer_norm_backward_workspace_size(int64_t n_rows, int32_t d, size_t* bytes) {
+  MOE_CHECK(check_rows(MOE_DTYPE_F32, n_rows, d, MOE_NORM_LAYER));
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "bytes is NULL");
+  size_t parts = 0;
+  for (int dtype : {MOE_DTYPE_F32, MOE_DTYPE_BF16}) {
+    const NormShape s = norm_shape(d, dtype, kNormGradVecs);
+    const size_t p = (size_t)norm_grad_grid(s, n_rows) * s.slots;
+    parts = p > parts ? p : parts;
+  }
+  *bytes = kAlign + align_up(parts * 2 * d * 4);
+  return MOE_OK;
+}
+
+#undef MOE_NORM_WIDE
+#define MOE_NORM_WIDE(F, T, ...)                                              \
+  if (s.W == 2) return F<T, 2, 2, VEC, LAY>(__VA_ARGS__);                     \
+  if (s.W == 4) return F<T, 4, 2, VEC, LAY>(__VA_ARGS__);                     \
+  if (s.W == 8) return F<T, 8, 2, VEC, LAY>(__VA_ARGS__);                     \
+  if (s.W == 16) return F<T, 16, 2, VEC, LAY>(__VA_ARGS__);                   \
+  if (s.W == 32 && s.NV <= 2) return F<T, 32, 2, VEC, LAY>(__VA_ARGS__);      \
+  if (s.W == 32) return F<T, 32, 4, VEC, LAY>(__VA_ARGS__);
+
+extern "C" moe_status moe_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_t n_rows, int32_t d,
+                                              int32_t kind, const float* gamma, const float* mean, const float* rstd,
+                                              const void* dres, void* dx, float* dgamma, float* dbeta, void* ws,
+                                              size_t ws_bytes, void* stream) {
+  MOE_CHECK(check_rows(dtype, n_rows, d, kind));
+  size_t need = 0;
+  MOE_CHECK(moe_layer_norm_backward_workspace_size(n_rows, d, &need));
+  MOE_ALIGNED4(gamma); MOE_ALIGNED4(mean); MOE_ALIGNED4(dgamma); MOE_ALIGNED4(dbeta);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (n_rows == 0) {
+    if (dgamma) cudaMemsetAsync(dgamma, 0, (size_t)d * 4, st);
+    if (dbeta) cudaMemsetAsync(dbeta, 0, (size_t)d * 4, st);
+    return cuda_status();
+  }
+  MOE_NONNULL(dy); MOE_NONNULL(x); MOE_NONNULL(dx); MOE_NONNULL4(rstd); MOE_ALIGNED(dres);
+  if (kind == MOE_NORM_LAYER && !mean) return fail(MOE_ERR_INVALID_ARG, "mean is NULL");
+  MOE_CHECK(check_ws(ws, ws_bytes, need));
+  const NormShape s = norm_shape(d, dtype, kNormGradVecs);
+  const int grid = norm_grad_grid(s, n_rows);
+  float* part = at<float>(ws, kAlign);
+  NormGradArgs a{dy, x, dres, gamma, mean, rstd, dx, part, n_rows, d, dgamma || dbeta};
+  const bool layer = kind == MOE_NORM_LAYER;
+  const bool vector = d % (dtype == MOE_DTYPE_F32 ? 4 : 8) == 0;
+  cudaError_t e = dtype == MOE_DTYPE_F32 ? MOE_NORM_PICK(start_norm_grad, float, a, s, grid, st)
+                                         : MOE_NORM_PICK(start_norm_grad, bf16, a, s, grid, st);
+  if (e == cudaSuccess && (dgamma || dbeta))
+    e = launch_pdl(norm_grad_sum_kernel, dim3((d + 31) / 32, 2), dim3(256), 0, st, part, grid * s.slots, d, dgamma, dbeta);
+  return e != cudaSuccess ? fail(MOE_ERR_CUDA, "norm backward launch: %s", cudaGetErrorString(e)) : MOE_OK;
+}

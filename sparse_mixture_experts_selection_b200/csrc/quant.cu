@@ -8,33 +8,12 @@
 // "GPUs, memory and failures" (serving notes) suggests lower-precision expert
 // weights when serving is bound by streaming them; the pages fix no format,
 // so the per-row power-of-two e4m3 layout is this library's reading.
-#include <cuda_fp8.h>
-
 #include "common.cuh"
+#include "e4m3.cuh"
 #include "kernels.h"
 
 namespace moe {
 namespace {
-
-// e with 2^e the smallest power of two such that amax <= 448 * 2^e, i.e. with
-// amax = M * 2^E (1 <= M < 2): e = E - 8 + [M > 1.75]; at least -126 (a normal
-// fp32 scale); 0 for amax == 0.
-__device__ __forceinline__ int pow2_exponent(float amax) {
-  const uint32_t b = __float_as_uint(amax) & 0x7FFFFFFFu;
-  if (b == 0) return 0;
-  int E;
-  uint32_t mant;
-  if ((b >> 23) == 0) {                        // subnormal amax
-    const int p = 31 - __clz(b);
-    E = p - 149;
-    mant = (b << (23 - p)) & 0x7FFFFFu;
-  } else {
-    E = (int)(b >> 23) - 127;
-    mant = b & 0x7FFFFFu;
-  }
-  const int e = E - 8 + (mant > 0x600000u ? 1 : 0);
-  return e < -126 ? -126 : e;
-}
 
 // Eight (bf16) or four (fp32) elements of one 16-byte load.
 __device__ __forceinline__ void load16(const uint16_t* p, float* v) {
@@ -86,8 +65,8 @@ quantize_rows_kernel(const TIn* __restrict__ src, const int32_t* __restrict__ sr
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, off));
-    const int e = pow2_exponent(amax);
-    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);      // 2^-e, exact
+    const int e = e4m3_scale_exponent(amax);
+    const float inv = pow2(-e);
     uint8_t* out = codes + r * cols;
     for (int c = lane * 16; c < cols; c += kWarp * 16) {
       float v[16];
@@ -95,16 +74,11 @@ quantize_rows_kernel(const TIn* __restrict__ src, const int32_t* __restrict__ sr
       for (int j = 0; j < 16; j += V) load16(row + c + j, v + j);
       uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i] * inv, v[4 * i + 1] * inv),
-                                                     __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2] * inv, v[4 * i + 3] * inv),
-                                                     __NV_SATFINITE, __NV_E4M3);
-        w[i] = (lo & 0xFFFFu) | (hi << 16);
-      }
+      for (int i = 0; i < 4; ++i)
+        w[i] = e4m3_pack4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
       *reinterpret_cast<uint4*>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    if (lane == 0) scales[r] = __uint_as_float((uint32_t)(e + 127) << 23);   // 2^e
+    if (lane == 0) scales[r] = pow2(e);
   }
 }
 
