@@ -488,8 +488,9 @@ moe_status moe_quantize_blocks(const void* src, int32_t src_dtype, int32_t n_mat
  *   or NULL for 1.  k a positive multiple of 16; n_cols >= 1; n_groups <= 1024.
  *   out [max_rows, n_cols], out_dtype MOE_DTYPE_BF16 or MOE_DTYPE_F32.  Rows
  *   outside [offsets[0], offsets[n_groups]) are left as they were.
- *   ws: its first 256 bytes zeroed once; offsets out of range set its error
- *   word (MOE_DEVERR_INDEX) and the group is skipped.
+ *   ws: its first 256 bytes zeroed once, and again after an error; offsets out
+ *   of order or out of range set its error word (MOE_DEVERR_INDEX) and nothing
+ *   is computed.  One workspace serves calls whose work does not overlap on the GPU.
  */
 moe_status moe_block_matmul_workspace_size(int32_t n_groups, int32_t n_cols, int32_t k,
                                            int32_t max_rows, size_t* bytes);

@@ -7,24 +7,33 @@
 // eight warps add it, times the two scales, to fp32 accumulators in their
 // registers, while the tensor cores fill the other tensor-memory buffer with the next block.
 //
-// Work unit = (group, 128-row tile, tile of 256 weight rows, range of blocks).
+// Work unit = (group, row tile of up to 128, tile of 256 weight rows, range of blocks).
 // The 256 weight rows are two blocks of 128: columns j .. j + 255 of the plain
 // product, or the gate and the up rows of the same 128 columns of the SwiGLU
-// product, whose epilogue then holds a whole 1 x 128 tile of each row of
-// A = SiLU(U) V and quantizes it on the spot: A never reaches memory but as
+// product, whose epilogue then holds whole 1 x 128 tiles of the rows of
+// A = SiLU(U) V and quantizes them on the spot: A never reaches memory but as
 // codes and scales.  Units of a group go row tile fastest, so CTAs that run
 // together share weight tiles through L2 and weights stream from HBM about once.
+//
+// A row tile of more than kSwapRows rows is the M = 128 operand and the weights are
+// N = 256.  A shorter one runs transposed: each block of weights is an M = 128 operand, the
+// rows rounded up to 16 are N.  The tensor cores, the loads and the accumulators then
+// do n / 128 of a tile's work instead of padding the rows, and a block takes one or
+// two of the four 128-column slots of tensor memory instead of always two, so up to four blocks are
+// on their way: a block waits about 1000 cycles on its barriers, twice its products.
 //
 // Few rows leave few units: the blocks of the reduction are then cut into ranges,
 // each unit of a range leaves its accumulators in the workspace, and the last
 // unit of a tile to finish adds the ranges in ascending order (so the sum
 // does not depend on which one was last) and runs the epilogue.
 //
-// Warp roles (384 threads): warp 0 = TMA producer (+ tensor memory), warp 1 =
-// MMA issuer, warps 4 .. 11 = accumulators and epilogue: warp w reads the tensor
-// memory lanes of rows 32 (w % 4) .. + 31 and one half of the columns.  A thread
-// of theirs holds 128 accumulators and 32 values on their way; the first four
-// warps give up registers for that (setmaxnreg).
+// Warp roles (384 threads): warp 0 = TMA producer (+ tensor memory), warp 1 = MMA
+// issuer, warps 2 and 3 = the scales of the next blocks, turned from rows of
+// blocks into blocks of rows in shared memory (read where they lie, a warp would
+// touch 32 lines a block), warps 4 .. 11 = accumulators and epilogue: warp w reads
+// the tensor memory lanes 32 (w % 4) .. + 31 and one half of the columns.  A
+// thread of theirs holds 128 accumulators and 32 values on their way; the first
+// four warps give up registers for that (setmaxnreg).
 #include <algorithm>
 #include <cuda.h>
 
@@ -38,11 +47,13 @@ namespace {
 
 constexpr int kBlock = 128;              // values per scale; also the k-block of a pipeline stage
 constexpr int kMaxGroups = 1024;
-constexpr int BM = 128, BN = 256;
-constexpr int A_BYTES = BM * kBlock, B_BYTES = BN * kBlock;
+constexpr int BM = 128, BN = 256;                   // rows and weight rows of a unit
+constexpr int A_BYTES = BM * kBlock, W_BYTES = kBlock * kBlock, B_BYTES = 2 * W_BYTES;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;      // 48 KB
 constexpr int STAGES = 4;
 constexpr int SUB_ROWS = 32;                        // row box of short row tiles
+constexpr int kSwapRows = 32;                       // row tiles of at most this many rows run transposed
+constexpr int SLOTS = 4, SLOT_COLS = 128;           // tensor memory
 constexpr int EPI_WARPS = 8;
 constexpr int NUM_THREADS = 128 + 32 * EPI_WARPS;
 constexpr int EPI_THREAD0 = 128;
@@ -51,18 +62,23 @@ constexpr int FEW_REGS = 72, MANY_REGS = 216;
 static_assert(128 * FEW_REGS + 32 * EPI_WARPS * MANY_REGS <= NUM_THREADS * 168, "registers of the launch");
 constexpr int TMEM_COLS = 512;
 constexpr int MAX_RANGES = 32;
+constexpr int CHUNK = 8;                            // blocks whose scales are staged together
 // byte counters of the tiles whose reduction is cut, in the control block of the
-// workspace: words 4 .. 63 (word 0 is the error word)
-constexpr int COUNTER_WORD0 = 4, MAX_CUT_TILES = 60 * 4;
-constexpr int PART_FLOATS = 128 * 32 * EPI_WARPS;   // accumulators of one unit
+// workspace: words 20 .. 63 (word 0 is the error word, 16 and 17 are the unit
+// counters of the layer's GEMMs, which may share the workspace)
+constexpr int COUNTER_WORD0 = 20, MAX_CUT_TILES = 44 * 4;
+constexpr int PART_FLOATS = 128 * 32 * EPI_WARPS;   // accumulators of a unit
 
 struct Control {
-  uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], drain;
+  float xs[2][CHUNK][BM];                           // scales of the rows, two chunks
+  float ws[2][2][CHUNK];                            // and of the two blocks of weight rows
+  uint64_t full[STAGES], done[STAGES], slot_empty[SLOTS], sc_full[2], sc_empty[2], drain;
   uint32_t tmem;
   int abort, last, total;
   int warp_sum[NUM_THREADS / 32];
-  float top[2][BM];                                 // SwiGLU: the two halves' row maxima
+  float top[4][BM];                                 // SwiGLU: maxima of the parts of a row's tile
   int prefix[kMaxGroups + 1];                       // units of the groups before
+  alignas(16) uint8_t piece[EPI_WARPS][32 * 64];    // a warp's 32 rows x 64 bytes on their way out
 };
 constexpr size_t SMEM_BYTES = (size_t)STAGES * STAGE_BYTES + sizeof(Control) + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
@@ -84,10 +100,13 @@ struct BlockArgs {
 };
 
 struct Unit {
-  int g, mt, nt, r0, rows;          // rows: of this tile
+  int g, nt, r0, rows;              // rows: of this tile
   int kb0, nk, range, tile;
+  int n16;                          // transposed: rows rounded up to 16, else 0
+  bool two;                         // both blocks of weight rows have columns
 };
 
+template <bool SWIGLU>
 __device__ __forceinline__ Unit decode(const BlockArgs& a, const int* prefix, int u) {
   int lo = 0, hi = a.G;             // prefix[lo] <= u < prefix[lo + 1]
   while (hi - lo > 1) {
@@ -103,31 +122,39 @@ __device__ __forceinline__ Unit decode(const BlockArgs& a, const int* prefix, in
   int local = u - prefix[lo];
   w.range = local % a.ranges;
   local /= a.ranges;
-  w.mt = local % mts;
   w.nt = local / mts;
-  w.r0 = r0 + w.mt * BM;
+  w.r0 = r0 + local % mts * BM;
   w.rows = min(BM, r1 - w.r0);
+  w.n16 = w.rows <= kSwapRows ? (w.rows + 15) & ~15 : 0;
+  w.two = SWIGLU || w.nt * BN + kBlock < a.N;
   w.kb0 = w.range * a.per;
   w.nk = min(a.KB, w.kb0 + a.per) - w.kb0;
   return w;
 }
 
-// Units before each group (prefix[G] = all) from the offsets; a group whose offsets
-// are out of order or out of range has none and sets the error word.
+// Units before each group (prefix[G] = all) from the offsets.  Offsets out of order
+// or out of range set the error word and leave no units: the tiles of ascending
+// offsets are at most those that the launch and the workspace were sized for.
 __device__ __forceinline__ void scan_groups(const BlockArgs& a, Control* c) {
   const int t = threadIdx.x, warp = t / kWarp, lane = t % kWarp;
   constexpr int PER = (kMaxGroups + NUM_THREADS - 1) / NUM_THREADS;
-  int n[PER], sum = 0;
+  int n[PER], sum = 0, bad = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int g = t * PER + i;
     n[i] = 0;
     if (g < a.G) {
       const int r0 = a.offsets ? __ldg(a.offsets + g) : 0, r1 = a.offsets ? __ldg(a.offsets + g + 1) : a.max_rows;
-      if (r0 < 0 || r1 < r0 || r1 > a.max_rows) set_device_error(a.ctrl, MOE_DEVERR_INDEX);
+      if (r0 < 0 || r1 < r0 || r1 > a.max_rows) bad = 1;
       else n[i] = (r1 - r0 + BM - 1) / BM * a.NT * a.ranges;
     }
     sum += n[i];
+  }
+  if (__syncthreads_or(bad)) {
+    if (t == 0) set_device_error(a.ctrl, MOE_DEVERR_INDEX);
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) n[i] = 0;
   }
   int inc = sum;
 #pragma unroll
@@ -148,6 +175,45 @@ __device__ __forceinline__ void scan_groups(const BlockArgs& a, Control* c) {
   __syncthreads();
 }
 
+// mbar_wait of common.cuh with the clock read only after many tries: these waits
+// come several times per block of 128.
+__device__ __forceinline__ bool block_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (*abort) return false;
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) {
+        set_device_error(err, MOE_DEVERR_WAIT_TIMEOUT);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// Where the next block's sums lie: slots are taken in turn, one block after the
+// other, by the MMA issuer and the accumulator warps alike.  A block of two slots takes two
+// neighbours (the odd slot before them is passed over); parity holds the phase bit of each slot.
+struct SlotWalk {
+  uint32_t next = 0, parity = 0;
+  // first slot of a block of n slots; its phase bits are flipped for the block after
+  __device__ __forceinline__ uint32_t take(uint32_t n, uint32_t& before) {
+    uint32_t s = next;
+    if (n == 2 && (s & 1u)) s = (s + 1) % SLOTS;
+    before = parity >> s;
+    parity ^= (n == 2 ? 3u : 1u) << s;
+    next = (s + n) % SLOTS;
+    return s;
+  }
+};
+
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // Wait without giving up on *abort (drains what is in flight before the CTA
 // releases its shared and tensor memory).
 __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity, int* err) {
@@ -156,83 +222,144 @@ __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity, int* 
     if (global_timer_ns() - t0 > kWaitLimitNs) { set_device_error(err, MOE_DEVERR_WAIT_TIMEOUT); return; }
 }
 
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  return (uint64_t)__float_as_uint(a) | ((uint64_t)__float_as_uint(b) << 32);
+// One lane of the (whole) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
 }
-__device__ __forceinline__ float low(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float high(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
-// acc += v * s, both halves
-__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t v, uint64_t s) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s));
+// 16 consecutive columns of this thread's tensor-memory lane: the load, and the wait
+// through which its values must pass before they are used.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :: "memory");
+}
+
+// a += v * s and b += w * s as one packed operation
+__device__ __forceinline__ void fma2(float& a, float& b, float v, float w, float s) {
+  asm("{\n\t.reg .b64 t, u, x;\n\t"
+      "mov.b64 t, {%0, %1};\n\tmov.b64 u, {%2, %3};\n\tmov.b64 x, {%4, %4};\n\t"
+      "fma.rn.f32x2 t, u, x, t;\n\t"
+      "mov.b64 {%0, %1}, t;\n\t}"
+      : "+f"(a), "+f"(b) : "f"(v), "f"(w), "f"(s));
+}
+
+// the same with a scale for each
+__device__ __forceinline__ void fma2(float& a, float& b, float v, float w, float s, float z) {
+  asm("{\n\t.reg .b64 t, u, x;\n\t"
+      "mov.b64 t, {%0, %1};\n\tmov.b64 u, {%2, %3};\n\tmov.b64 x, {%4, %5};\n\t"
+      "fma.rn.f32x2 t, u, x, t;\n\t"
+      "mov.b64 {%0, %1}, t;\n\t}"
+      : "+f"(a), "+f"(b) : "f"(v), "f"(w), "f"(s), "f"(z));
+}
+
+// Barrier of the 256 accumulator threads; true when all of them bring true.
+__device__ __forceinline__ bool all_agree(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 6, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all) : "r"((uint32_t)ok) : "memory");
+  return all != 0;
 }
 
 __device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
 
-// Plain epilogue: this thread's row of the output, columns col0 .. col0 + 127.
-__device__ __forceinline__ void store_row(const BlockArgs& a, const uint64_t (&acc)[64], int row, int col0) {
-  const float rs = a.row_scale ? __ldg(a.row_scale + row) : 1.0f;
-  const size_t base = (size_t)row * a.N + col0;
-  const bool whole = col0 + 128 <= a.N;
-  if (a.out_f32) {
-    float* o = static_cast<float*>(a.out) + base;
-    if (whole && a.N % 4 == 0) {
+// 16 bytes `v` (0 .. 3) of a row of the piece: turned by the row, so that neither
+// the rows written nor those read meet in a bank
+__device__ __forceinline__ uint4* piece_at(uint8_t* piece, int row, int v) {
+  return reinterpret_cast<uint4*>(piece + row * 64 + ((v ^ (row >> 1)) & 3) * 16);
+}
+
+// Plain epilogue: columns col0 .. col0 + 127 of the warp's rows row0 .. row0 + n - 1,
+// one row a lane.  Stored as they lie, a 16-byte store of a warp would touch 32
+// lines (4000 cycles a tile were measured); so 64 bytes of each row at a time go through
+// shared memory and leave four (or, for rows of odd alignment, 16 or 32) lanes to a row.
+template <typename T>
+__device__ __forceinline__ void store_rows(const BlockArgs& a, const float (&acc)[128], uint8_t* piece, int row0, int n,
+                                           int col0) {
+  constexpr int PER = 64 / (int)sizeof(T);         // columns of a piece
+  const int lane = threadIdx.x % kWarp;
+  const float rs = a.row_scale && lane < n ? __ldg(a.row_scale + row0 + lane) : 1.0f;
+  T* out = static_cast<T*>(a.out) + (size_t)row0 * a.N + col0;
+  const bool vectors = a.N % (16 / (int)sizeof(T)) == 0;
 #pragma unroll
-      for (int j = 0; j < 64; j += 2)
-        *reinterpret_cast<float4*>(o + 2 * j) =
-            make_float4(low(acc[j]) * rs, high(acc[j]) * rs, low(acc[j + 1]) * rs, high(acc[j + 1]) * rs);
-    } else {
+  for (int p = 0; p < 128 / PER; ++p) {
+    const int cols = min(PER, a.N - col0 - p * PER);
+    if (cols <= 0) break;
 #pragma unroll
-      for (int j = 0; j < 64; ++j) {
-        if (col0 + 2 * j < a.N) o[2 * j] = low(acc[j]) * rs;
-        if (col0 + 2 * j + 1 < a.N) o[2 * j + 1] = high(acc[j]) * rs;
-      }
-    }
-    return;
-  }
-  bf16* o = static_cast<bf16*>(a.out) + base;
-  if (whole && a.N % 8 == 0) {
-#pragma unroll
-    for (int j = 0; j < 64; j += 4) {
-      uint32_t p[4];
+    for (int v = 0; v < 4; ++v) {
+      uint32_t q[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(low(acc[j + i]) * rs, high(acc[j + i]) * rs);
-        p[i] = *reinterpret_cast<const uint32_t*>(&v);
+        if constexpr (sizeof(T) == 4) {
+          q[i] = __float_as_uint(acc[p * PER + 4 * v + i] * rs);
+        } else {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(acc[p * PER + 8 * v + 2 * i] * rs, acc[p * PER + 8 * v + 2 * i + 1] * rs);
+          q[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
       }
-      *reinterpret_cast<uint4*>(o + 2 * j) = make_uint4(p[0], p[1], p[2], p[3]);
+      *piece_at(piece, lane, v) = make_uint4(q[0], q[1], q[2], q[3]);
     }
-  } else {
+    __syncwarp();
+    if (vectors) {
+      const int v = lane % 4;                      // whole vectors: cols is a multiple of 16 / sizeof(T)
 #pragma unroll
-    for (int j = 0; j < 64; ++j) {
-      if (col0 + 2 * j < a.N) o[2 * j] = from_f32<bf16>(low(acc[j]) * rs);
-      if (col0 + 2 * j + 1 < a.N) o[2 * j + 1] = from_f32<bf16>(high(acc[j]) * rs);
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + lane / 4;
+        if (r < n && v * (16 / (int)sizeof(T)) < cols)
+          *reinterpret_cast<uint4*>(out + (size_t)r * a.N + p * PER + v * (16 / (int)sizeof(T))) = *piece_at(piece, r, v);
+      }
+    } else {
+      constexpr int VALS = 16 / (int)sizeof(T);
+      const int j = lane % PER;
+#pragma unroll 4
+      for (int r = lane / PER; r < n; r += kWarp / PER)
+        if (j < cols) out[(size_t)r * a.N + p * PER + j] = reinterpret_cast<const T*>(piece_at(piece, r, j / VALS))[j % VALS];
     }
+    __syncwarp();
   }
 }
 
-// SwiGLU epilogue: this thread holds 64 gate (acc[0 .. 31]) and the same 64 up
-// columns (acc[32 .. 63]) of its row; the other 64 columns of the 1 x 128 tile are
-// with the warp of the other half, which shares the maximum through shared memory.
-__device__ __forceinline__ void store_swiglu(const BlockArgs& a, const uint64_t (&acc)[64], const Unit& w, int r,
-                                             int half, Control* c) {
-  float v[64], top = 0.0f;
+// SwiGLU epilogue: this thread holds 64 gate (acc[0 .. 63]) and the same 64 up
+// columns (acc[64 .. 127]) of its row, which become their products; the other 64 columns of
+// the 1 x 128 tile are with the warp of the other half, which shares the maximum
+// through shared memory.
+__device__ __forceinline__ void store_swiglu(const BlockArgs& a, float (&acc)[128], const Unit& w, int row0, int rows,
+                                             int r, int half, Control* c) {
+  float top = 0.0f;
   const int col0 = w.nt * kBlock + half * 64;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    v[2 * j] = col0 + 2 * j < a.N ? silu(low(acc[j])) * low(acc[32 + j]) : 0.0f;
-    v[2 * j + 1] = col0 + 2 * j + 1 < a.N ? silu(high(acc[j])) * high(acc[32 + j]) : 0.0f;
-    top = fmaxf(top, fmaxf(fabsf(v[2 * j]), fabsf(v[2 * j + 1])));
+  for (int j = 0; j < 64; ++j) {
+    acc[j] = col0 + j < a.N ? silu(acc[j]) * acc[64 + j] : 0.0f;
+    top = fmaxf(top, fabsf(acc[j]));
   }
   const int quad = r / 32;
   c->top[half][r] = top;
-  asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
+  asm volatile("bar.sync %0, 64;" ::"r"(8 + quad) : "memory");
   top = fmaxf(top, c->top[half ^ 1][r]);
-  asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
-  if (r >= w.rows) return;
+  asm volatile("bar.sync %0, 64;" ::"r"(8 + quad) : "memory");
+  if (r >= rows) return;
   const int e = e4m3_scale_exponent(top);
   const float inv = pow2(-e);
-  const size_t row = (size_t)(w.r0 + r);
+  const size_t row = (size_t)(row0 + r);
   uint8_t* o = static_cast<uint8_t*>(a.out) + row * a.N + col0;
 #pragma unroll
   for (int j = 0; j < 64; j += 16) {
@@ -240,10 +367,59 @@ __device__ __forceinline__ void store_swiglu(const BlockArgs& a, const uint64_t 
     uint32_t q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      q[i] = e4m3_pack4(v[j + 4 * i] * inv, v[j + 4 * i + 1] * inv, v[j + 4 * i + 2] * inv, v[j + 4 * i + 3] * inv);
+      q[i] = e4m3_pack4(acc[j + 4 * i] * inv, acc[j + 4 * i + 1] * inv, acc[j + 4 * i + 2] * inv, acc[j + 4 * i + 3] * inv);
     *reinterpret_cast<uint4*>(o + j) = make_uint4(q[0], q[1], q[2], q[3]);
   }
   if (half == 0) a.out_scale[row * a.NB + w.nt] = pow2(e);
+}
+
+// Transposed tiles: the thread holds columns col (acc[t]) and col + 128 (acc[64 + t])
+// of rows row0 + t, t < n; a warp writes 32 neighbouring columns of a row at a time.
+template <typename T>
+__device__ __forceinline__ void store_columns(const BlockArgs& a, const float (&acc)[128], int row0, int n, int col) {
+  const int lane = threadIdx.x % kWarp;
+  // lane t holds the scales of rows t and t + 32
+  const float rs0 = a.row_scale && lane < n ? __ldg(a.row_scale + row0 + lane) : 1.0f;
+  const float rs1 = a.row_scale && lane + 32 < n ? __ldg(a.row_scale + row0 + lane + 32) : 1.0f;
+  T* out = static_cast<T*>(a.out) + (size_t)row0 * a.N + col;
+#pragma unroll
+  for (int t = 0; t < 64; ++t) {
+    if (t >= n) break;
+    const float rs = __shfl_sync(kFull, t < 32 ? rs0 : rs1, t % 32);
+    if (col < a.N) out[(size_t)t * a.N] = from_f32<T>(acc[t] * rs);
+    if (col + kBlock < a.N) out[(size_t)t * a.N + kBlock] = from_f32<T>(acc[64 + t] * rs);
+  }
+}
+
+// Transposed SwiGLU: acc[t] is the gate and acc[64 + t] the up value of column col
+// of row row0 + t; the tile's 128 columns are the 128 lanes of the four warps
+// of this half of the rows, which share their maxima through shared memory.
+__device__ __forceinline__ void store_swiglu_columns(const BlockArgs& a, float (&acc)[128], const Unit& w, int row0,
+                                                     int t0, int n, int r, int half, Control* c) {
+  const int col = w.nt * kBlock + r, quad = r / 32;
+#pragma unroll
+  for (int t = 0; t < 64; ++t) {
+    if (t >= n) break;
+    acc[t] = col < a.N ? silu(acc[t]) * acc[64 + t] : 0.0f;
+    // magnitudes order like their bits; a NaN does not count
+    const uint32_t top = __reduce_max_sync(kFull, acc[t] == acc[t] ? __float_as_uint(fabsf(acc[t])) : 0u);
+    if (r % 32 == 0) c->top[quad][t0 + t] = __uint_as_float(top);
+  }
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+#pragma unroll
+  for (int t = 0; t < 64; ++t) {
+    if (t >= n) break;
+    float top = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) top = fmaxf(top, c->top[q][t0 + t]);
+    const int e = e4m3_scale_exponent(top);
+    const size_t row = (size_t)(row0 + t);
+    if (col < a.N)
+      static_cast<uint8_t*>(a.out)[row * a.N + col] =
+          (uint8_t)__nv_cvt_float_to_fp8(acc[t] * pow2(-e), __NV_SATFINITE, __NV_E4M3);
+    if (r == 0) a.out_scale[row * a.NB + w.nt] = pow2(e);
+  }
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");   // the maxima are rewritten by the next unit
 }
 
 template <bool SWIGLU>
@@ -255,16 +431,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
   Control* c = reinterpret_cast<Control*>(smem + STAGES * STAGE_BYTES);
   volatile int* abort_flag = &c->abort;
   int* err = a.ctrl;
-  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  // the same in all lanes, and known to be: the roles' loops then run on the uniform path
+  const int warp = __shfl_sync(kFull, (int)threadIdx.x / kWarp, 0), lane = threadIdx.x % kWarp;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return block_wait(bar, parity, abort_flag, err); };
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) { mbar_init(&c->full[s], 1); mbar_init(&c->empty[s], 1); }
-    for (int b = 0; b < 2; ++b) { mbar_init(&c->acc_full[b], 1); mbar_init(&c->acc_empty[b], EPI_WARPS); }
+    for (int s = 0; s < STAGES; ++s) { mbar_init(&c->full[s], 1); mbar_init(&c->done[s], 1); }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&c->sc_full[b], 2 * kWarp); mbar_init(&c->sc_empty[b], EPI_WARPS);
+    }
+    for (int b = 0; b < SLOTS; ++b) mbar_init(&c->slot_empty[b], EPI_WARPS);
     mbar_init(&c->drain, 1);
     c->abort = 0;
     fence_barrier_init();
   }
-  if (warp == 0) tmem_alloc(&c->tmem, TMEM_COLS);
   if (warp == 1 && lane == 0) { prefetch_tmap(&a.x); prefetch_tmap(&a.x32); prefetch_tmap(&a.w0); prefetch_tmap(&a.w1); }
+  __syncthreads();
+  if (warp == 0) tmem_alloc(&c->tmem, TMEM_COLS);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -278,58 +460,116 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FEW_REGS));
     if (warp == 0 && lane == 0) {
       // ---------------- TMA producer ----------------
-      int stage = 0, issued = 0;
+      int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-        const Unit w = decode(a, c->prefix, u);
-        const int sub = w.rows > BM - SUB_ROWS ? 0 : (w.rows + SUB_ROWS - 1) / SUB_ROWS;
+        const Unit w = decode<SWIGLU>(a, c->prefix, u);
+        const int sub = (w.rows + SUB_ROWS - 1) / SUB_ROWS;       // four boxes of 32 rows are one of 128
+        const uint32_t tx = (uint32_t)(sub * SUB_ROWS * kBlock + (w.two ? 2 : 1) * W_BYTES);
         const int by = w.g * a.N + w.nt * (SWIGLU ? kBlock : BN);
-        const bool two = SWIGLU || w.nt * BN + kBlock < a.N;
-        const uint32_t tx = (uint32_t)(sub ? sub * SUB_ROWS * kBlock : A_BYTES) + (two ? B_BYTES : B_BYTES / 2);
         for (int i = 0; i < w.nk; ++i) {
-          if (!mbar_wait(&c->empty[stage], phase ^ 1u, abort_flag, err)) { ok = false; break; }
+          if (!wait(&c->done[stage], phase ^ 1u)) { ok = false; break; }
           const int k = (w.kb0 + i) * kBlock;
           mbar_arrive_expect_tx(&c->full[stage], tx);
           // the weights first: they come from HBM, the rows mostly from L2
           tma_load_2d(sB + stage * B_BYTES, &a.w0, &c->full[stage], k, by);
-          if (two) tma_load_2d(sB + stage * B_BYTES + B_BYTES / 2, &a.w1, &c->full[stage], k, SWIGLU ? by : by + kBlock);
-          if (sub == 0) tma_load_2d(sA + stage * A_BYTES, &a.x, &c->full[stage], k, w.r0);
-          for (int q = 0; q < sub; ++q)
-            tma_load_2d(sA + stage * A_BYTES + q * SUB_ROWS * kBlock, &a.x32, &c->full[stage], k, w.r0 + q * SUB_ROWS);
-          ++issued;
+          if (w.two) tma_load_2d(sB + stage * B_BYTES + W_BYTES, &a.w1, &c->full[stage], k, SWIGLU ? by : by + kBlock);
+          if (sub == BM / SUB_ROWS) {
+            tma_load_2d(sA + stage * A_BYTES, &a.x, &c->full[stage], k, w.r0);
+          } else {
+            for (int q = 0; q < sub; ++q)
+              tma_load_2d(sA + stage * A_BYTES + q * SUB_ROWS * kBlock, &a.x32, &c->full[stage], k, w.r0 + q * SUB_ROWS);
+          }
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      // the last loads must have landed before shared memory is released
-      for (int i = 0; i < STAGES && i < issued; ++i) {
-        if (--stage < 0) { stage = STAGES - 1; phase ^= 1u; }
-        wait_drain(&c->full[stage], phase, err);
+      // every stage's last release has arrived (the loads have landed and been read)
+      // before this CTA may leave
+      for (int i = 0; i < STAGES && ok; ++i) {
+        ok = wait(&c->done[stage], phase ^ 1u);
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // ---------------- MMA issuer ----------------
+      const uint64_t descA = sdesc_kmajor_sw128(smem_u32(sA)), descB = sdesc_kmajor_sw128(smem_u32(sB));
       int stage = 0;
-      uint32_t phase = 0, it = 0;          // it: blocks so far; buffer it % 2
+      uint32_t phase = 0;
+      SlotWalk walk;
       bool ok = true;
       for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-        const Unit w = decode(a, c->prefix, u);
-        const uint32_t idesc = idesc_e4m3_f32(BM, SWIGLU || w.nt * BN + kBlock < a.N ? BN : kBlock);
-        for (int i = 0; i < w.nk; ++i, ++it) {
-          const uint32_t buf = it & 1u;
-          if (!mbar_wait(&c->acc_empty[buf], ((it >> 1) & 1u) ^ 1u, abort_flag, err) ||
-              !mbar_wait(&c->full[stage], phase, abort_flag, err)) { ok = false; break; }
+        const Unit w = decode<SWIGLU>(a, c->prefix, u);
+        const uint32_t n_slots = w.n16 == 0 || w.n16 > SLOT_COLS / 2 ? 2u : 1u;
+        const uint32_t idesc = w.n16 ? idesc_e4m3_f32(BM, w.n16) : idesc_e4m3_f32(BM, w.two ? BN : kBlock);
+        const uint32_t second = n_slots * (SLOT_COLS / 2);     // transposed: columns of the second block of weights
+        for (int i = 0; i < w.nk; ++i) {
+          uint32_t before;
+          const uint32_t s = walk.take(n_slots, before);
+          ok = wait(&c->full[stage], phase) && wait(&c->slot_empty[s], (before & 1u) ^ 1u) &&
+               (n_slots == 1 || wait(&c->slot_empty[s + 1], ((before >> 1) & 1u) ^ 1u));
+          if (!__all_sync(kFull, ok)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(sA + stage * A_BYTES), b0 = smem_u32(sB + stage * B_BYTES);
+          // descriptors count 16 bytes; a block of 128 is four steps of 32
+          const uint64_t da = descA + stage * (A_BYTES / 16), db = descB + stage * (B_BYTES / 16);
+          const uint32_t d = tmem + s * SLOT_COLS;
+          if (elect_one()) {
+            if (w.n16 == 0) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_e4m3(tmem + buf * BN, sdesc_kmajor_sw128(a0 + 32 * k), sdesc_kmajor_sw128(b0 + 32 * k), idesc, k != 0);
-          tc_commit(&c->empty[stage]);
-          tc_commit(&c->acc_full[buf]);
+              for (int k = 0; k < 4; ++k) tc_mma_e4m3(d, da + 2 * k, db + 2 * k, idesc, k != 0);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) tc_mma_e4m3(d, db + 2 * k, da + 2 * k, idesc, k != 0);
+              if (w.two) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tc_mma_e4m3(d + second, db + W_BYTES / 16 + 2 * k, da + 2 * k, idesc, k != 0);
+              }
+            }
+            tc_commit(&c->done[stage]);          // the stage is read and the sums are there
+          }
+          __syncwarp();
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      tc_commit(&c->drain);
+      if (elect_one()) tc_commit(&c->drain);
+      __syncwarp();
       wait_drain(&c->drain, 0, err);
+    } else if (warp >= 2) {
+      // ---------------- scales ----------------
+      const int t = threadIdx.x - 2 * kWarp;
+      uint32_t ch = 0;                     // chunks so far; buffer ch % 2
+      bool ok = true;
+      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+        const Unit w = decode<SWIGLU>(a, c->prefix, u);
+        const int j0 = SWIGLU ? w.nt : 2 * w.nt, j1 = SWIGLU ? w.nt : min(j0 + 1, a.NB - 1);
+        for (int c0 = 0; c0 < w.nk; c0 += CHUNK, ++ch) {
+          const uint32_t b = ch & 1u;
+          const int n = min(CHUNK, w.nk - c0), k = w.kb0 + c0;
+          if (!wait(&c->sc_empty[b], ((ch >> 1) & 1u) ^ 1u)) { ok = false; break; }
+          for (int r = t; r < w.rows; r += 2 * kWarp) {
+            const float* p = a.xs + (size_t)(w.r0 + r) * a.KB + k;
+            if (n == CHUNK && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+              float4 v[CHUNK / 4];
+#pragma unroll
+              for (int i = 0; i < CHUNK / 4; ++i) v[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
+#pragma unroll
+              for (int i = 0; i < CHUNK / 4; ++i) {
+                c->xs[b][4 * i][r] = v[i].x; c->xs[b][4 * i + 1][r] = v[i].y;
+                c->xs[b][4 * i + 2][r] = v[i].z; c->xs[b][4 * i + 3][r] = v[i].w;
+              }
+            } else {
+              float v[CHUNK];
+#pragma unroll
+              for (int i = 0; i < CHUNK; ++i) v[i] = i < n ? __ldg(p + i) : 0.0f;
+#pragma unroll
+              for (int i = 0; i < CHUNK; ++i) c->xs[b][i][r] = v[i];
+            }
+          }
+          if (t < 2 * CHUNK && t % CHUNK < n)
+            c->ws[b][t / CHUNK][t % CHUNK] =
+                __ldg((t < CHUNK ? a.ws0 : a.ws1) + ((size_t)w.g * a.NB + (t < CHUNK ? j0 : j1)) * a.KB + k + t % CHUNK);
+          mbar_arrive(&c->sc_full[b]);
+        }
+      }
     }
   } else {
     // ---------------- accumulators and epilogue ----------------
@@ -337,56 +577,106 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
     const int quad = warp & 3, half = (warp - 4) / 4;
     const int r = quad * 32 + lane;
     const int t = threadIdx.x - EPI_THREAD0;
-    uint32_t it = 0;
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t release = smem_u32(&c->slot_empty[0]);           // slot s: + 8 s
+    int stage = 0;
+    uint32_t phase = 0, ch = 0;
+    SlotWalk walk;
     bool ok = true;
     for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-      const Unit w = decode(a, c->prefix, u);
-      // warps without rows, or without columns, only keep the buffers moving
-      const bool idle = quad * 32 >= w.rows || (!SWIGLU && w.nt * BN + half * kBlock >= a.N);
-      const float* xs = a.xs + (size_t)(w.r0 + min(r, w.rows - 1)) * a.KB + w.kb0;
-      const float* s0 = a.ws0 + ((size_t)w.g * a.NB + (SWIGLU ? w.nt : min(2 * w.nt + half, a.NB - 1))) * a.KB + w.kb0;
-      const float* s1 = SWIGLU ? a.ws1 + ((size_t)w.g * a.NB + w.nt) * a.KB + w.kb0 : s0;
-      // tensor-memory columns of the thread's 128: gate and up of half the tile, or one half of the columns
-      const uint32_t base = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(half * (SWIGLU ? 64 : 128));
-      constexpr int SECOND = SWIGLU ? kBlock : 64;   // the last 64 columns, from `base`
-      uint64_t acc[64];
+      const Unit w = decode<SWIGLU>(a, c->prefix, u);
+      const bool swap = w.n16 != 0;
+      // transposed: this half's rows t0 .. t0 + n - 1 of the tile, 16 at a time
+      const int t0 = half ? (w.n16 + 31) / 32 * 16 : 0;
+      const int chunks = swap ? (half ? w.n16 - t0 : (w.n16 + 31) / 32 * 16) / 16 : 0;
+      const int n = swap ? max(0, min(w.rows - t0, 16 * chunks)) : 0;
+      const uint32_t n_slots = !swap || w.n16 > SLOT_COLS / 2 ? 2u : 1u;
+      const uint32_t second = n_slots * (SLOT_COLS / 2);
+      // warps without rows, or without columns, only keep the slots moving
+      const bool idle = swap ? chunks == 0 : quad * 32 >= w.rows || (half == 1 && !w.two);
+      float acc[128];
 #pragma unroll
-      for (int j = 0; j < 64; ++j) acc[j] = 0;
-      // scales are loaded two blocks ahead of their use
-      float x0 = __ldg(xs), g0 = __ldg(s0), u0 = SWIGLU ? __ldg(s1) : 0.0f;
-      float x1 = 0.0f, g1 = 0.0f, u1 = 0.0f;
-      if (w.nk > 1) { x1 = __ldg(xs + 1); g1 = __ldg(s0 + 1); if (SWIGLU) u1 = __ldg(s1 + 1); }
-      for (int i = 0; i < w.nk; ++i, ++it) {
-        float x2 = 0.0f, g2 = 0.0f, u2 = 0.0f;
-        if (i + 2 < w.nk) { x2 = __ldg(xs + i + 2); g2 = __ldg(s0 + i + 2); if (SWIGLU) u2 = __ldg(s1 + i + 2); }
-        const uint32_t buf = it & 1u;
-        if (!mbar_wait(&c->acc_full[buf], (it >> 1) & 1u, abort_flag, err)) { ok = false; break; }
+      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+      for (int i = 0; i < w.nk; ++i) {
+        const uint32_t sb = ch & 1u;
+        uint32_t before;
+        const uint32_t s = walk.take(n_slots, before);
+        if (i % CHUNK == 0 && !__all_sync(kFull, wait(&c->sc_full[sb], (ch >> 1) & 1u))) { ok = false; break; }
+        const float w0 = c->ws[sb][0][i % CHUNK], w1 = c->ws[sb][1][i % CHUNK];
+        const float x = swap ? 0.0f : c->xs[sb][i % CHUNK][r];
+        if (!__all_sync(kFull, wait(&c->done[stage], phase))) { ok = false; break; }
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         tc_fence_after();
-        if (!idle) {
-          const float sg = x0 * g0, su = SWIGLU ? x0 * u0 : sg;
+        const uint32_t d = lane_base + s * SLOT_COLS;
+        auto free_slots = [&] {                       // all values are in registers
+          tc_fence_before();
+          if (lane == 0) {
+            arrive_at(release + 8u * s);
+            if (n_slots == 2) arrive_at(release + 8u * s + 8u);
+          }
+        };
+        if (idle) {
+          free_slots();
+        } else if (!swap) {
+          // the thread's row, 128 columns: a block of the plain product, or 64 gate and their 64 up columns
+          const uint32_t base = d + (uint32_t)(half * (SWIGLU ? 64 : 128));
+          const float s_first = x * (SWIGLU || half == 0 ? w0 : w1), s_last = SWIGLU ? x * w1 : s_first;
+          // 16 columns arrive while the 16 before are added
+          uint32_t v[2][16];
+          tmem_ld16(base, v[0]);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            tmem_wait16(v[q & 1]);
+            if (q < 7) tmem_ld16(base + 16 * (q + 1) + (SWIGLU && q + 1 >= 4 ? 64 : 0), v[(q + 1) & 1]);
+            else free_slots();
+            const float sc = q < 4 ? s_first : s_last;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2)
+              fma2(acc[16 * q + j], acc[16 * q + j + 1], __uint_as_float(v[q & 1][j]), __uint_as_float(v[q & 1][j + 1]), sc);
+          }
+        } else {
+          // one column of each block of weights, 16 rows at a time
+          const float* xs = &c->xs[sb][i % CHUNK][t0];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            float v[32];
-            tmem_ld32(base + buf * BN + (q < 2 ? 32 * q : SECOND + 32 * (q - 2)), v);
-            const float s = q < 2 ? sg : su;
-            const uint64_t ss = pack2(s, s);
+            if (q < chunks) {
+              uint32_t v0[16], v1[16];
+              tmem_ld16(d + t0 + 16 * q, v0);
+              tmem_ld16(d + second + t0 + 16 * q, v1);
+              tmem_wait16(v0);
+              tmem_wait16(v1);
+              if (q == chunks - 1) free_slots();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) fma2(acc[16 * q + j], pack2(v[2 * j], v[2 * j + 1]), ss);
+              for (int j = 0; j < 16; j += 4) {
+                const float4 xv = *reinterpret_cast<const float4*>(xs + 16 * q + j);
+                const int p = 16 * q + j;
+                fma2(acc[p], acc[p + 1], __uint_as_float(v0[j]), __uint_as_float(v0[j + 1]), xv.x * w0, xv.y * w0);
+                fma2(acc[p + 2], acc[p + 3], __uint_as_float(v0[j + 2]), __uint_as_float(v0[j + 3]), xv.z * w0, xv.w * w0);
+                fma2(acc[64 + p], acc[65 + p], __uint_as_float(v1[j]), __uint_as_float(v1[j + 1]), xv.x * w1, xv.y * w1);
+                fma2(acc[66 + p], acc[67 + p], __uint_as_float(v1[j + 2]), __uint_as_float(v1[j + 3]), xv.z * w1, xv.w * w1);
+              }
+            }
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c->acc_empty[buf]);
-        x0 = x1; x1 = x2; g0 = g1; g1 = g2; u0 = u1; u1 = u2;
+        if (i % CHUNK == CHUNK - 1 || i == w.nk - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c->sc_empty[sb]);
+          ++ch;
+        }
       }
+      // the barriers below want every warp: if a wait gave up in one, all leave here
+      if (SWIGLU || a.ranges > 1) ok = all_agree(ok);
       if (!ok) break;
       if (a.ranges > 1) {
         // leave the accumulators; the last range of the tile to arrive adds them in order
-        float4* mine = reinterpret_cast<float4*>(a.part + ((size_t)w.tile * a.ranges + w.range) * PART_FLOATS);
-        if (!idle && r < w.rows)
+        const bool mine = !idle && (swap || r < w.rows);
+        const size_t tile = (size_t)w.tile * a.ranges;
+        float4* here = reinterpret_cast<float4*>(a.part + (tile + w.range) * PART_FLOATS);
+        if (mine)
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            __stcg(mine + j * 256 + t, make_float4(low(acc[2 * j]), high(acc[2 * j]), low(acc[2 * j + 1]), high(acc[2 * j + 1])));
+            if (!swap || 4 * j % 64 < n)
+              __stcg(here + j * 256 + t, make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]));
         __threadfence();
         asm volatile("bar.sync 5, 256;" ::: "memory");
         if (t == 0) {
@@ -401,26 +691,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
         const bool last = c->last != 0;
         asm volatile("bar.sync 5, 256;" ::: "memory");
         if (!last) continue;
-        if (!idle && r < w.rows) {
+        if (mine) {
 #pragma unroll
-          for (int j = 0; j < 64; ++j) acc[j] = 0;
+          for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
           for (int q = 0; q < a.ranges; ++q) {
-            const float4* p = reinterpret_cast<const float4*>(a.part + ((size_t)w.tile * a.ranges + q) * PART_FLOATS);
-            const uint64_t one = pack2(1.0f, 1.0f);
+            const float4* p = reinterpret_cast<const float4*>(a.part + (tile + q) * PART_FLOATS);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
+              if (swap && 4 * j % 64 >= n) continue;
               const float4 v = __ldcg(p + j * 256 + t);
-              fma2(acc[2 * j], pack2(v.x, v.y), one);
-              fma2(acc[2 * j + 1], pack2(v.z, v.w), one);
+              acc[4 * j] += v.x; acc[4 * j + 1] += v.y; acc[4 * j + 2] += v.z; acc[4 * j + 3] += v.w;
             }
           }
         }
       }
       if constexpr (SWIGLU) {
-        if (!idle) store_swiglu(a, acc, w, r, half, c);
+        if (swap) {
+          if (!idle) store_swiglu_columns(a, acc, w, w.r0 + t0, t0, n, r, half, c);
+        } else if (!idle) {
+          store_swiglu(a, acc, w, w.r0, w.rows, r, half, c);
+        }
       } else {
-        if (!idle && r < w.rows) store_row(a, acc, w.r0 + r, w.nt * BN + half * kBlock);
+        if (swap) {
+          if (!idle) {
+            if (a.out_f32) store_columns<float>(a, acc, w.r0 + t0, n, w.nt * BN + r);
+            else store_columns<bf16>(a, acc, w.r0 + t0, n, w.nt * BN + r);
+          }
+        } else if (!idle) {
+          uint8_t* piece = c->piece[warp - 4];
+          const int row0 = w.r0 + quad * 32, rows = min(32, w.rows - quad * 32), col0 = w.nt * BN + half * kBlock;
+          if (a.out_f32) store_rows<float>(a, acc, piece, row0, rows, col0);
+          else store_rows<bf16>(a, acc, piece, row0, rows, col0);
+        }
       }
+    }
+  }
+  if (*abort_flag) {
+    // loads and MMAs may be in flight still: give them time to land before the
+    // shared and tensor memory goes
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 1000000ull) {
     }
   }
   tc_fence_before();
@@ -456,8 +766,8 @@ bool tensor_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, 
 }
 
 // How a product is cut: tiles is an upper bound of the (row, column) tiles of
-// any offsets; when they leave more than half of the SMs idle the blocks of the
-// reduction are cut into ranges, at least two blocks each.
+// any offsets; when they leave more than half of the SMs idle the blocks of
+// the reduction are cut into ranges, at least two blocks each.
 struct Cut {
   int nt, ranges, per;
   int64_t tiles;
@@ -497,7 +807,7 @@ cudaError_t product(int G, int N, int K, int max_rows, const int* offsets, const
   a.KB = blocks_of(K); a.NB = blocks_of(N); a.NT = cut.nt;
   a.ranges = cut.ranges; a.per = cut.per;
   a.offsets = offsets;
-  a.xs = o.xs; a.ws0 = o.ws0; a.ws1 = o.ws1; a.row_scale = o.row_scale;
+  a.xs = o.xs; a.ws0 = o.ws0; a.ws1 = swiglu ? o.ws1 : o.ws0; a.row_scale = o.row_scale;
   a.out_f32 = out_f32; a.out = out; a.out_scale = out_scale; a.part = part; a.ctrl = ctrl;
   static bool attr_done[64] = {};
   int dev = 0, sms = 0;
@@ -510,7 +820,7 @@ cudaError_t product(int G, int N, int K, int max_rows, const int* offsets, const
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_done[dev] = true;
   }
-  const unsigned grid = (unsigned)std::min<int64_t>(cut.tiles * cut.ranges, sms > 0 ? sms : 1);
+  const unsigned grid = (unsigned)std::min<int64_t>(cut.tiles * cut.ranges, std::max(sms, 1));
   return launch_pdl(swiglu ? block_product_kernel<true> : block_product_kernel<false>, dim3(grid), dim3(NUM_THREADS),
                     SMEM_BYTES, st, a);
 }
@@ -523,6 +833,9 @@ moe_status check_product(int n_groups, int n_cols, int k, int max_rows) {
   if (max_rows < 0) return fail(MOE_ERR_INVALID_ARG, "max_rows=%d < 0", max_rows);
   if (n_cols > 1 << 20 || k > 1 << 20) return fail(MOE_ERR_UNSUPPORTED, "n_cols=%d k=%d above 2^20", n_cols, k);
   if ((int64_t)n_groups * n_cols > 0x7FFFFFFF) return fail(MOE_ERR_UNSUPPORTED, "n_groups * n_cols above 2^31");
+  // units are counted in 32 bits: row tiles x column tiles (of at least 128 columns)
+  if (((int64_t)max_rows / BM + n_groups) * blocks_of(n_cols) > 0x3FFFFFFF)
+    return fail(MOE_ERR_UNSUPPORTED, "max_rows=%d with n_cols=%d: too many tiles", max_rows, n_cols);
   return MOE_OK;
 }
 
