@@ -310,57 +310,49 @@ def moe_clear_device_error(ws, stream=None) -> None:
 # ---------------------------------------------------------------------------
 # around and inside a sublayer x + dropout(MoE(norm(x)))
 # ---------------------------------------------------------------------------
-def _tensors(**checks):
-    """The device of a call's tensors (None without any) after a check of them:
-    name=(tensor, dtypes, number of values).  The
-    kernels take dense arrays by pointer, so a strided view, another type, a short
-    tensor or one of another device is refused here.  Plain addresses pass."""
+# types that are taken, by torch's names (torch is imported with the first call)
+_F32, _I32S, _BF16S = ("float32",), ("int32",), ("bfloat16",)
+_CODES, _RNG, _BYTES = ("uint8", "float8_e4m3fn"), ("int64", "uint64"), ("uint8",)
+_ACT = {DTYPE_F32: _F32, DTYPE_BF16: _BF16S}
+_torch = None
+_types = {(): ()}                  # names -> torch dtypes; no names: an unknown dtype code, nothing matches
+
+
+def _call(fn, stream, checks, *args) -> None:
+    """Check the tensors of a call -- (name, tensor, type names, number of values)
+    -- and make it on their device.  The kernels take dense arrays by pointer, so a
+    strided view, another type, a short tensor or one of another device is
+    refused here.  None and plain addresses pass."""
+    global _torch
+    if _torch is None:
+        import torch as _torch
     device = other = None
-    for name, (t, dtypes, n) in checks.items():
-        if t is None or isinstance(t, int):
+    for name, t, names, n in checks:
+        if t is None or t.__class__ is int:
             continue
+        types = _types.get(names)
+        if types is None:
+            types = _types[names] = tuple(getattr(_torch, k) for k in names)
+        if t.dtype not in types:
+            raise MoeError(1, f"{name} has type {t.dtype}, not {' or '.join(names)}")
         if not t.is_contiguous():
             raise MoeError(1, f"{name} is not contiguous")
-        if t.element_size() != dtypes[0] or str(t.dtype) not in dtypes:
-            raise MoeError(1, f"{name} has type {t.dtype}, not {' or '.join(map(str, dtypes[1:]))}")
         if t.numel() < n:
             raise MoeError(1, f"{name} has {t.numel()} values, {n} are needed")
+        at = t.get_device()
         if device is None:
-            device = t.device
-        elif t.device != device:
-            other = f"{name} is on {t.device}, another tensor on {device}"
-    if device is not None and device.type != "cuda":
-        other = f"tensors are on {device}, not on a GPU"
-    if other:
-        raise MoeError(1, other)
-    return device
-
-
-class _On:
-    """Make a tensor's device current while a call enqueues its work."""
-
-    def __init__(self, device):
-        import torch
-        self.guard = (torch.cuda.device(device)
-                      if device is not None and device.index != torch.cuda.current_device() else None)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-# the size of a value and the types that are taken
-_F32 = (4, "torch.float32")
-_I32S = (4, "torch.int32")
-_ACT = {DTYPE_F32: _F32, DTYPE_BF16: (2, "torch.bfloat16")}
-_NONE = (0,)                       # an unknown dtype code: no tensor matches
-_CODES = (1, "torch.uint8", "torch.float8_e4m3fn")
-_RNG = (8, "torch.int64", "torch.uint64")
-_BYTES = (1, "torch.uint8")
+            device = at
+        elif at != device:
+            other = name
+    if other is not None or (device is not None and device < 0):
+        raise MoeError(1, "the tensors are not on one GPU" + (f" ({other} is on another device)" if other else ""))
+    if device is None or device == _torch.cuda.current_device():
+        status = fn(*args, _stream(stream))
+    else:
+        with _torch.cuda.device(device):
+            status = fn(*args, _stream(stream))
+    if status != 0:
+        raise MoeError(status, lib().moe_last_error_detail().decode())
 
 
 def _blocks(n: int) -> int:
@@ -371,14 +363,12 @@ def moe_layer_norm(x, dtype: int, n_rows: int, d: int, kind: int, gamma, beta, e
                    codes=None, scales=None, stream=None):
     """Norm of n_rows rows of d values (NORM_LAYER or NORM_RMS); with codes and
     scales the output once more in e4m3 tiles of 1 x 128 (see include/moe.h)."""
-    n, act = n_rows * d, _ACT.get(dtype, _NONE)
-    dev = _tensors(x=(x, act, n), gamma=(gamma, _F32, d), beta=(beta, _F32, d), out=(out, act, n),
-                   mean=(mean, _F32, n_rows), rstd=(rstd, _F32, n_rows), codes=(codes, _CODES, n),
-                   scales=(scales, _F32, n_rows * _blocks(d)))
-    with _On(dev):
-        _check(lib().moe_layer_norm(_ptr(x), int(dtype), int(n_rows), int(d), int(kind), _ptr(gamma), _ptr(beta),
-                                    float(eps), _ptr(out), _ptr(mean), _ptr(rstd), _ptr(codes), _ptr(scales),
-                                    _stream(stream)))
+    n, act = n_rows * d, _ACT.get(dtype, ())
+    _call(lib().moe_layer_norm, stream, (("x", x, act, n), ("gamma", gamma, _F32, d), ("beta", beta, _F32, d),
+          ("out", out, act, n), ("mean", mean, _F32, n_rows), ("rstd", rstd, _F32, n_rows),
+          ("codes", codes, _CODES, n), ("scales", scales, _F32, n_rows * _blocks(d))),
+          _ptr(x), int(dtype), int(n_rows), int(d), int(kind), _ptr(gamma), _ptr(beta), float(eps), _ptr(out),
+          _ptr(mean), _ptr(rstd), _ptr(codes), _ptr(scales))
 
 
 def moe_layer_norm_backward_workspace_size(n_rows: int, d: int) -> int:
@@ -390,52 +380,43 @@ def moe_layer_norm_backward_workspace_size(n_rows: int, d: int) -> int:
 def moe_layer_norm_backward(dy, x, dtype: int, n_rows: int, d: int, kind: int, gamma, mean, rstd, dres, dx, dgamma,
                             dbeta, ws, stream=None):
     """Gradients of moe_layer_norm; dres is added to dx (see include/moe.h)."""
-    n, act = n_rows * d, _ACT.get(dtype, _NONE)
-    dev = _tensors(dy=(dy, act, n), x=(x, act, n), gamma=(gamma, _F32, d), mean=(mean, _F32, n_rows),
-                   rstd=(rstd, _F32, n_rows), dres=(dres, act, n), dx=(dx, act, n), dgamma=(dgamma, _F32, d),
-                   dbeta=(dbeta, _F32, d), ws=(ws, _BYTES, 0))
-    with _On(dev):
-        _check(lib().moe_layer_norm_backward(
-            _ptr(dy), _ptr(x), int(dtype), int(n_rows), int(d), int(kind), _ptr(gamma), _ptr(mean), _ptr(rstd),
-            _ptr(dres), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(ws), ws.numel(), _stream(stream)))
+    n, act = n_rows * d, _ACT.get(dtype, ())
+    _call(lib().moe_layer_norm_backward, stream, (("dy", dy, act, n), ("x", x, act, n), ("gamma", gamma, _F32, d),
+          ("mean", mean, _F32, n_rows), ("rstd", rstd, _F32, n_rows), ("dres", dres, act, n), ("dx", dx, act, n),
+          ("dgamma", dgamma, _F32, d), ("dbeta", dbeta, _F32, d), ("ws", ws, _BYTES, 0)),
+          _ptr(dy), _ptr(x), int(dtype), int(n_rows), int(d), int(kind), _ptr(gamma), _ptr(mean), _ptr(rstd),
+          _ptr(dres), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(ws), ws.numel())
 
 
 def moe_dropout_add(x, res, dtype: int, n: int, p: float, rng, out, stream=None):
     """out = res + dropout(x) over n values; rng: int64 [2] on the device, the
     seed and the number of this draw (see include/moe.h)."""
-    act = _ACT.get(dtype, _NONE)
-    dev = _tensors(x=(x, act, n), res=(res, act, n), rng=(rng, _RNG, 2), out=(out, act, n))
-    with _On(dev):
-        _check(lib().moe_dropout_add(_ptr(x), _ptr(res), int(dtype), int(n), float(p), _ptr(rng), _ptr(out),
-                                     _stream(stream)))
+    act = _ACT.get(dtype, ())
+    _call(lib().moe_dropout_add, stream, (("x", x, act, n), ("res", res, act, n), ("rng", rng, _RNG, 2),
+          ("out", out, act, n)),
+          _ptr(x), _ptr(res), int(dtype), int(n), float(p), _ptr(rng), _ptr(out))
 
 
 def moe_dropout_backward(dy, dtype: int, n: int, p: float, rng, dx, stream=None):
     """dx = dy through the mask that moe_dropout_add drew with the same rng, p and n."""
-    act = _ACT.get(dtype, _NONE)
-    dev = _tensors(dy=(dy, act, n), rng=(rng, _RNG, 2), dx=(dx, act, n))
-    with _On(dev):
-        _check(lib().moe_dropout_backward(_ptr(dy), int(dtype), int(n), float(p), _ptr(rng), _ptr(dx),
-                                          _stream(stream)))
+    act = _ACT.get(dtype, ())
+    _call(lib().moe_dropout_backward, stream, (("dy", dy, act, n), ("rng", rng, _RNG, 2), ("dx", dx, act, n)),
+          _ptr(dy), int(dtype), int(n), float(p), _ptr(rng), _ptr(dx))
 
 
 def moe_quantize_tiles(src, src_dtype: int, n_rows: int, cols: int, codes, scales, stream=None):
     """e4m3 codes and one power-of-two scale for each 1 x 128 tile of the rows."""
-    dev = _tensors(src=(src, _ACT.get(src_dtype, _NONE), n_rows * cols), codes=(codes, _CODES, n_rows * cols),
-                   scales=(scales, _F32, n_rows * _blocks(cols)))
-    with _On(dev):
-        _check(lib().moe_quantize_tiles(_ptr(src), int(src_dtype), int(n_rows), int(cols), _ptr(codes), _ptr(scales),
-                                        _stream(stream)))
+    _call(lib().moe_quantize_tiles, stream, (("src", src, _ACT.get(src_dtype, ()), n_rows * cols),
+          ("codes", codes, _CODES, n_rows * cols), ("scales", scales, _F32, n_rows * _blocks(cols))),
+          _ptr(src), int(src_dtype), int(n_rows), int(cols), _ptr(codes), _ptr(scales))
 
 
 def moe_quantize_blocks(src, src_dtype: int, n_mats: int, rows: int, cols: int, codes, scales, stream=None):
     """e4m3 codes and one power-of-two scale for each 128 x 128 block of the matrices."""
     n = n_mats * rows * cols
-    dev = _tensors(src=(src, _ACT.get(src_dtype, _NONE), n), codes=(codes, _CODES, n),
-                   scales=(scales, _F32, n_mats * _blocks(rows) * _blocks(cols)))
-    with _On(dev):
-        _check(lib().moe_quantize_blocks(_ptr(src), int(src_dtype), int(n_mats), int(rows), int(cols), _ptr(codes),
-                                         _ptr(scales), _stream(stream)))
+    _call(lib().moe_quantize_blocks, stream, (("src", src, _ACT.get(src_dtype, ()), n),
+          ("codes", codes, _CODES, n), ("scales", scales, _F32, n_mats * _blocks(rows) * _blocks(cols))),
+          _ptr(src), int(src_dtype), int(n_mats), int(rows), int(cols), _ptr(codes), _ptr(scales))
 
 
 def moe_block_matmul_workspace_size(n_groups: int, n_cols: int, k: int, max_rows: int) -> int:
@@ -448,15 +429,13 @@ def moe_block_matmul(n_groups: int, n_cols: int, k: int, max_rows: int, offsets,
                      out_dtype: int, out, ws, stream=None):
     """Grouped product of block-scaled e4m3 operands (see include/moe.h); offsets
     None with one group takes all max_rows rows."""
-    dev = _tensors(offsets=(offsets, _I32S, n_groups + 1), x=(x, _CODES, max_rows * k),
-                   x_scale=(x_scale, _F32, max_rows * _blocks(k)), w=(w, _CODES, n_groups * n_cols * k),
-                   w_scale=(w_scale, _F32, n_groups * _blocks(n_cols) * _blocks(k)),
-                   row_scale=(row_scale, _F32, max_rows), out=(out, _ACT.get(out_dtype, _NONE), max_rows * n_cols),
-                   ws=(ws, _BYTES, 0))
-    with _On(dev):
-        _check(lib().moe_block_matmul(int(n_groups), int(n_cols), int(k), int(max_rows), _ptr(offsets), _ptr(x),
-                                      _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(row_scale), int(out_dtype),
-                                      _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+    _call(lib().moe_block_matmul, stream, (("offsets", offsets, _I32S, n_groups + 1), ("x", x, _CODES, max_rows * k),
+          ("x_scale", x_scale, _F32, max_rows * _blocks(k)), ("w", w, _CODES, n_groups * n_cols * k),
+          ("w_scale", w_scale, _F32, n_groups * _blocks(n_cols) * _blocks(k)),
+          ("row_scale", row_scale, _F32, max_rows), ("out", out, _ACT.get(out_dtype, ()), max_rows * n_cols),
+          ("ws", ws, _BYTES, 0)),
+          int(n_groups), int(n_cols), int(k), int(max_rows), _ptr(offsets), _ptr(x), _ptr(x_scale), _ptr(w),
+          _ptr(w_scale), _ptr(row_scale), int(out_dtype), _ptr(out), _ptr(ws), ws.numel())
 
 
 def moe_block_ffn_workspace_size(n_experts: int, d_model: int, d_ffn: int, max_rows: int) -> int:
@@ -471,13 +450,12 @@ def moe_block_ffn(n_experts: int, d_model: int, d_ffn: int, max_rows: int, offse
     """Grouped SwiGLU experts on block-scaled e4m3 weights (see include/moe.h)."""
     n = n_experts * d_model * d_ffn
     nb = n_experts * _blocks(d_model) * _blocks(d_ffn)
-    dev = _tensors(offsets=(offsets, _I32S, n_experts + 1), x=(x, _CODES, max_rows * d_model),
-                   x_scale=(x_scale, _F32, max_rows * _blocks(d_model)), w_gate=(w_gate, _CODES, n),
-                   s_gate=(s_gate, _F32, nb), w_up=(w_up, _CODES, n), s_up=(s_up, _F32, nb),
-                   w_down=(w_down, _CODES, n), s_down=(s_down, _F32, nb), row_scale=(row_scale, _F32, max_rows),
-                   out=(out, _ACT.get(out_dtype, _NONE), max_rows * d_model), ws=(ws, _BYTES, 0))
-    with _On(dev):
-        _check(lib().moe_block_ffn(int(n_experts), int(d_model), int(d_ffn), int(max_rows), _ptr(offsets), _ptr(x),
-                                   _ptr(x_scale), _ptr(w_gate), _ptr(s_gate), _ptr(w_up), _ptr(s_up), _ptr(w_down),
-                                   _ptr(s_down), _ptr(row_scale), int(out_dtype), _ptr(out), _ptr(ws), ws.numel(),
-                                   _stream(stream)))
+    _call(lib().moe_block_ffn, stream, (("offsets", offsets, _I32S, n_experts + 1),
+          ("x", x, _CODES, max_rows * d_model), ("x_scale", x_scale, _F32, max_rows * _blocks(d_model)),
+          ("w_gate", w_gate, _CODES, n), ("s_gate", s_gate, _F32, nb), ("w_up", w_up, _CODES, n),
+          ("s_up", s_up, _F32, nb), ("w_down", w_down, _CODES, n), ("s_down", s_down, _F32, nb),
+          ("row_scale", row_scale, _F32, max_rows), ("out", out, _ACT.get(out_dtype, ()), max_rows * d_model),
+          ("ws", ws, _BYTES, 0)),
+          int(n_experts), int(d_model), int(d_ffn), int(max_rows), _ptr(offsets), _ptr(x), _ptr(x_scale),
+          _ptr(w_gate), _ptr(s_gate), _ptr(w_up), _ptr(s_up), _ptr(w_down), _ptr(s_down), _ptr(row_scale),
+          int(out_dtype), _ptr(out), _ptr(ws), ws.numel())

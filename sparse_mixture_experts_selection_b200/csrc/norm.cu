@@ -21,7 +21,14 @@ namespace moe {
 namespace {
 
 constexpr int kMaxNormCols = 16384;
-constexpr int kNormGrid = 2 * 148;       // blocks of the backward: their partial sums are the workspace
+constexpr int kSms = 148;
+constexpr int kNormGrid = 2 * kSms;      // blocks of the row-by-row backward: their partial sums are the workspace
+// Wide rows of long batches run in resident blocks that walk the rows, the next
+// kDepth rows on their way to shared memory meanwhile: see ring_norm_kernel.
+constexpr int kDepth = 3;
+constexpr int grad_depth(int W) { return W == 32 ? 2 : 4; }    // of the backward: 192 KB
+constexpr int kRingRows = 4 * kSms;      // fewer rows: one block per row has the shorter way
+constexpr int kRingVecs = 128;           // rows of at most this many 16-byte vectors fit one or two warps
 
 // How rows map to warps: W warps per row, NV vectors of V elements per lane,
 // `slots` rows at a time in a block of `threads`.
@@ -84,6 +91,8 @@ template <typename T, int W, bool VECTOR>
 struct Row {
   static constexpr int N = Vec<T>::N, L = 32 * W;
   __device__ static int col(int i, int j, int lane) { return VECTOR ? (i * L + lane) * N + j : (i * N + j) * L + lane; }
+  // whole vectors are inside or outside together
+  __device__ static bool inside(int i, int j, int lane, int d) { return col(i, VECTOR ? 0 : j, lane) < d; }
   // columns at or beyond d read as `other`
   __device__ static void load(const T* p, int d, int i, int lane, float other, float (&v)[N]) {
     if (VECTOR) {
@@ -158,14 +167,14 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float (*buf)[32 * K], int
 #pragma unroll
     for (int k = 0; k < K; ++k) b[k * 32 + warp] = v[k];
   __syncthreads();
-  const int w0 = warp / W * W;
+  // lane l takes the sum of warp l % W of the row; W is a power of two
+  const int from = warp / W * W + threadIdx.x % W;
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    float s = 0.0f;
+  for (int k = 0; k < K; ++k) v[k] = b[k * 32 + from];
 #pragma unroll
-    for (int w = 0; w < W; ++w) s += b[k * 32 + w0 + w];
-    v[k] = s;
-  }
+  for (int off = W / 2; off > 0; off >>= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(kFull, v[k], off);
   gen ^= 1;
 }
 
@@ -181,23 +190,15 @@ struct NormArgs {
   float eps;
 };
 
+// One row, in the registers of its W warps (r >= n_rows: only the barriers are kept).
 template <typename T, int W, int NV, bool VECTOR, bool LAYER, bool TILES>
-__global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W) norm_kernel(const NormArgs a) {
+__device__ __forceinline__ void normalize(const NormArgs& a, float (&v)[NV][Vec<T>::N], int64_t r, int lane, float inv_d,
+                                          const float (&g)[NV][Vec<T>::N], const float (&b)[NV][Vec<T>::N],
+                                          float (*buf)[32], int& gen) {
   using R = Row<T, W, VECTOR>;
-  constexpr int N = R::N, L = R::L, SLOTS = (W <= 8 ? 256 : 32 * W) / L;
-  __shared__ float buf[2][32];
-  int gen = 0;
-  pdl_wait();
-  pdl_trigger();
-  const int lane = threadIdx.x % L;
-  const int64_t r = (int64_t)blockIdx.x * SLOTS + threadIdx.x / L;
-  const bool valid = r < a.n_rows;
+  constexpr int N = R::N, L = R::L;
   const int d = a.d;
-  const T* x = static_cast<const T*>(a.x) + (valid ? r : 0) * d;
-  float v[NV][N];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) R::load(x, d, i, lane, 0.0f, v[i]);
-  const float inv_d = 1.0f / (float)d;
+  const bool valid = r < a.n_rows;
   float mean = 0.0f;
   if (LAYER) {
     float s[1] = {0.0f};
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W) norm_kernel(const NormA
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      if (LAYER) v[i][j] = R::col(i, j, lane) < d ? v[i][j] - mean : 0.0f;
+      if (LAYER) v[i][j] -= R::inside(i, j, lane, d) ? mean : 0.0f;     // beyond the row: 0 - 0
       q[0] = fmaf(v[i][j], v[i][j], q[0]);
     }
   row_sum<W, 1>(q, buf, gen);
@@ -224,11 +225,8 @@ __global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W) norm_kernel(const NormA
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    float g[N], b[N];
-    R::load_f32(a.gamma, d, i, lane, 1.0f, g);
-    R::load_f32(a.beta, d, i, lane, 0.0f, b);
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[i][j] = fmaf(v[i][j] * rstd, g[j], b[j]);
+    for (int j = 0; j < N; ++j) v[i][j] = fmaf(v[i][j] * rstd, g[i][j], b[i][j]);
     if (valid && a.out) R::store(static_cast<T*>(a.out) + r * d, d, i, lane, v[i]);
     if (TILES) {
       // the stored values, in tiles of 128 columns = 128 / N neighbouring lanes
@@ -255,6 +253,28 @@ __global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W) norm_kernel(const NormA
       }
     }
   }
+}
+
+template <typename T, int W, int NV, bool VECTOR, bool LAYER, bool TILES>
+__global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W) norm_kernel(const NormArgs a) {
+  using R = Row<T, W, VECTOR>;
+  constexpr int N = R::N, L = R::L, SLOTS = (W <= 8 ? 256 : 32 * W) / L;
+  __shared__ float buf[2][32];
+  int gen = 0;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x % L;
+  const int64_t r = (int64_t)blockIdx.x * SLOTS + threadIdx.x / L;
+  const int d = a.d;
+  const T* x = static_cast<const T*>(a.x) + (r < a.n_rows ? r : 0) * d;
+  float v[NV][N], g[NV][N], b[NV][N];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    R::load(x, d, i, lane, 0.0f, v[i]);
+    R::load_f32(a.gamma, d, i, lane, 1.0f, g[i]);
+    R::load_f32(a.beta, d, i, lane, 0.0f, b[i]);
+  }
+  normalize<T, W, NV, VECTOR, LAYER, TILES>(a, v, r, lane, 1.0f / (float)d, g, b, buf, gen);
 }
 
 struct NormGradArgs {
@@ -305,7 +325,7 @@ __global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W) norm_grad_kernel(const 
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        if (R::col(i, j, lane) >= d) { xh[i][j] = 0.0f; continue; }
+        if (!R::inside(i, j, lane, d)) { xh[i][j] = 0.0f; continue; }
         xh[i][j] = (xh[i][j] - mean) * rstd;
         if (valid) {
           dg[i][j] = fmaf(dy[i][j], xh[i][j], dg[i][j]);
@@ -341,11 +361,179 @@ __global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W) norm_grad_kernel(const 
     }
 }
 
+// ---------------------------------------------------------------------------
+// wide rows, long batches
+// ---------------------------------------------------------------------------
+// Each thread copies its own two vectors of a row to its own place in shared
+// memory (cp.async, past the L1 cache) kDepth rows ahead, so nothing but the sums is
+// shared between threads, the loads in flight do not wait for the sums, and
+// gains stay in registers.  One block per row instead reads the gains again with each
+// row and has no load in flight while it sums: 47 against 27 us for 4096 x 7168 bf16
+// (4.3 TB/s; a plain copy of that size takes 21 us), and depth 4 or 6 takes 31 or 33.
+// What bounds it now is issuing: 20 instructions a value, 69 % of the slots.
+__device__ __forceinline__ void copy16(void* smem, const void* global, bool in) {
+  const int bytes = in ? 16 : 0;                       // 0: zeros are written
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem)), "l"(global), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+constexpr int kRingNV = 2;
+
+template <typename T, int W, bool LAYER, bool TILES>
+__global__ void __launch_bounds__(32 * W, W <= 16 ? 32 / W : 1) ring_norm_kernel(const NormArgs a) {
+  using R = Row<T, W, true>;
+  constexpr int N = R::N, L = R::L, NV = kRingNV;
+  extern __shared__ uint4 ring[];                      // [kDepth][NV][L]
+  __shared__ float buf[2][32];
+  int gen = 0;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x, d = a.d;
+  const T* x = static_cast<const T*>(a.x);
+  auto fetch = [&](int64_t r, int slot) {
+    if (r < a.n_rows) {
+      const int64_t at = r * d + lane * N;
+      uint4* to = ring + slot * (NV * L) + lane;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const bool in = R::col(i, 0, lane) < d;
+        copy16(to + i * L, x + (in ? at + i * L * N : 0), in);
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < kDepth - 1; ++k) fetch(blockIdx.x + (int64_t)k * gridDim.x, k);
+  float g[NV][N], b[NV][N];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    R::load_f32(a.gamma, d, i, lane, 1.0f, g[i]);
+    R::load_f32(a.beta, d, i, lane, 0.0f, b[i]);
+  }
+  const float inv_d = 1.0f / (float)d;
+  int slot = 0;
+  for (int64_t r = blockIdx.x; r < a.n_rows; r += gridDim.x) {
+    fetch(r + (int64_t)(kDepth - 1) * gridDim.x, (slot + kDepth - 1) % kDepth);
+    copy_wait<kDepth - 1>();
+    float v[NV][N];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) Vec<T>::unpack(ring[(slot * NV + i) * L + lane], v[i]);
+    slot = slot + 1 == kDepth ? 0 : slot + 1;
+    normalize<T, W, NV, true, LAYER, TILES>(a, v, r, lane, inv_d, g, b, buf, gen);
+  }
+}
+
+// The backward: gains, the running dgamma and dbeta and the row in registers, one block
+// of 512 threads on an SM: 44 us for 4096 x 7168 bf16 with dres (5.4 TB/s), and 4 for
+// the parts' sums.  The row read twice from shared memory with 1024 threads on an SM
+// took 41 instructions a value instead of 28 and 64 us, 1024 threads with one vector
+// each 73 us.
+template <typename T, int W, bool LAYER>
+__global__ void __launch_bounds__(32 * W, W <= 16 ? 16 / W : 1) ring_norm_grad_kernel(const NormGradArgs a) {
+  using R = Row<T, W, true>;
+  constexpr int N = R::N, L = R::L, NV = kRingNV, DEPTH = grad_depth(W);
+  extern __shared__ uint4 ring[];                      // [DEPTH][dy, x, dres][NV][L]
+  __shared__ float buf[2][64];
+  int gen = 0;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x, d = a.d;
+  const int arrays = a.dres ? 3 : 2;
+  const T *dy_ = static_cast<const T*>(a.dy), *x_ = static_cast<const T*>(a.x), *dres_ = static_cast<const T*>(a.dres);
+  auto fetch = [&](int64_t r, int slot) {
+    if (r < a.n_rows) {
+      const int64_t at = r * d + lane * N;
+      uint4* to = ring + slot * (3 * NV * L) + lane;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const bool in = R::col(i, 0, lane) < d;
+        const int64_t c = in ? at + i * L * N : 0;
+        copy16(to + i * L, dy_ + c, in);
+        copy16(to + (NV + i) * L, x_ + c, in);
+        if (arrays == 3) copy16(to + (2 * NV + i) * L, dres_ + c, in);
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < DEPTH - 1; ++k) fetch(blockIdx.x + (int64_t)k * gridDim.x, k);
+  float gamma[NV][N], dg[NV][N], db[NV][N];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    R::load_f32(a.gamma, d, i, lane, 1.0f, gamma[i]);
+#pragma unroll
+    for (int j = 0; j < N; ++j) dg[i][j] = db[i][j] = 0.0f;
+  }
+  const float inv_d = 1.0f / (float)d;
+  int slot = 0;
+  float next_rstd = 0.0f, next_mean = 0.0f;            // a row ahead, like the row itself
+  if (blockIdx.x < a.n_rows) {
+    next_rstd = a.rstd[blockIdx.x];
+    if (LAYER) next_mean = a.mean[blockIdx.x];
+  }
+  for (int64_t r = blockIdx.x; r < a.n_rows; r += gridDim.x) {
+    fetch(r + (int64_t)(DEPTH - 1) * gridDim.x, (slot + DEPTH - 1) % DEPTH);
+    const float rstd = next_rstd, mean = next_mean;
+    if (r + gridDim.x < a.n_rows) {
+      next_rstd = a.rstd[r + gridDim.x];
+      if (LAYER) next_mean = a.mean[r + gridDim.x];
+    }
+    copy_wait<DEPTH - 1>();
+    const uint4* from = ring + slot * (3 * NV * L) + lane;
+    float dy[NV][N], xh[NV][N], s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      Vec<T>::unpack(from[i * L], dy[i]);              // zeros beyond the row: they add nothing
+      Vec<T>::unpack(from[(NV + i) * L], xh[i]);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        xh[i][j] = (xh[i][j] - mean) * rstd;
+        dg[i][j] = fmaf(dy[i][j], xh[i][j], dg[i][j]);
+        db[i][j] += dy[i][j];
+        dy[i][j] *= gamma[i][j];
+        s[0] += dy[i][j];
+        s[1] = fmaf(dy[i][j], xh[i][j], s[1]);
+      }
+    }
+    row_sum<W, 2>(s, buf, gen);
+    // rstd (g - m1 - xhat m2) as (rstd g - rstd m1) - xhat (rstd m2)
+    const float m1 = LAYER ? s[0] * inv_d * rstd : 0.0f, m2 = s[1] * inv_d * rstd;
+    T* dx = static_cast<T*>(a.dx) + r * d;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float o[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) o[j] = fmaf(-xh[i][j], m2, LAYER ? fmaf(dy[i][j], rstd, -m1) : dy[i][j] * rstd);
+      if (arrays == 3) {
+        float res[N];
+        Vec<T>::unpack(from[(2 * NV + i) * L], res);
+#pragma unroll
+        for (int j = 0; j < N; ++j) o[j] += res[j];
+      }
+      R::store(dx, d, i, lane, o);
+    }
+    slot = slot + 1 == DEPTH ? 0 : slot + 1;
+  }
+  if (!a.want_sums) return;
+  float* part = a.part + (size_t)blockIdx.x * 2 * d;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = R::col(i, 0, lane);
+    if (c >= d) continue;
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      *reinterpret_cast<float4*>(part + c + j) = make_float4(dg[i][j], dg[i][j + 1], dg[i][j + 2], dg[i][j + 3]);
+      *reinterpret_cast<float4*>(part + d + c + j) = make_float4(db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3]);
+    }
+  }
+}
+
 // dgamma (blockIdx.y = 0) and dbeta (1): the parts summed in a fixed order, 32
-// columns per block, eight interleaved runs of parts joined at the end.
-__global__ void __launch_bounds__(256) norm_grad_sum_kernel(const float* part, int parts, int d,
-                                                            float* dgamma, float* dbeta) {
-  __shared__ float s[8][33];
+// columns per block, 32 interleaved runs of parts joined at the end.
+__global__ void __launch_bounds__(1024) norm_grad_sum_kernel(const float* part, int parts, int d, float* dgamma,
+                                                             float* dbeta) {
+  __shared__ float s[32][33];
   pdl_wait();
   pdl_trigger();
   float* out = blockIdx.y == 0 ? dgamma : dbeta;
@@ -354,15 +542,15 @@ __global__ void __launch_bounds__(256) norm_grad_sum_kernel(const float* part, i
   const int c = blockIdx.x * 32 + cx;
   float v = 0.0f;
   if (c < d)
-    for (int p = py; p < parts; p += 8) v += part[((size_t)p * 2 + blockIdx.y) * d + c];
+#pragma unroll 4
+    for (int p = py; p < parts; p += 32) v += part[((size_t)p * 2 + blockIdx.y) * d + c];
   s[py][cx] = v;
   __syncthreads();
-  if (py == 0 && c < d) {
-    float t = 0.0f;
+  // warp py holds column py's runs
+  v = s[cx][py];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) t += s[k][cx];
-    out[c] = t;
-  }
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(kFull, v, off);
+  if (cx == 0 && blockIdx.x * 32 + py < d) out[blockIdx.x * 32 + py] = v;
 }
 
 template <typename T, int W, int NV, bool VECTOR, bool LAYER>
@@ -377,6 +565,54 @@ cudaError_t start_norm(const NormArgs& a, const NormShape& s, cudaStream_t st) {
 template <typename T, int W, int NV, bool VECTOR, bool LAYER>
 cudaError_t start_norm_grad(const NormGradArgs& a, const NormShape& s, int grid, cudaStream_t st) {
   return launch_pdl(norm_grad_kernel<T, W, NV, VECTOR, LAYER>, dim3(grid), dim3(s.threads), 0, st, a);
+}
+
+// Warps per row of the resident blocks, 0 where one block per row (or warp) runs.
+int ring_warps(int64_t n_rows, int d, int dtype) {
+  const int V = dtype == MOE_DTYPE_F32 ? 4 : 8;
+  if (n_rows < kRingRows || d % V || d / V <= kRingVecs || d / V > 32 * 32 * kRingNV) return 0;
+  int W = 4;
+  while (d / V > 32 * W * kRingNV) W *= 2;
+  return W;
+}
+int ring_grad_grid(int W) { return W >= 16 ? kSms : kSms * 16 / W; }    // 512 threads of an SM
+
+// 48 KB of static and dynamic shared memory need no permission
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+  return bytes <= 47 * 1024 ? cudaSuccess
+                            : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <typename T, int W, bool LAYER, bool TILES>
+cudaError_t start_ring(const NormArgs& a, cudaStream_t st) {
+  const size_t smem = (size_t)kDepth * kRingNV * 32 * W * 16;
+  const int per_sm = W <= 16 ? 32 / W : 1;             // 1024 threads, 128 KB at most
+  const dim3 grid((unsigned)(a.n_rows < kSms * per_sm ? a.n_rows : kSms * per_sm));
+  const cudaError_t e = allow_smem(ring_norm_kernel<T, W, LAYER, TILES>, smem);
+  return e != cudaSuccess ? e : launch_pdl(ring_norm_kernel<T, W, LAYER, TILES>, grid, dim3(32 * W), smem, st, a);
+}
+template <typename T, int W, bool LAYER>
+cudaError_t start_ring(const NormArgs& a, cudaStream_t st) {
+  return a.codes ? start_ring<T, W, LAYER, true>(a, st) : start_ring<T, W, LAYER, false>(a, st);
+}
+template <typename T, bool LAYER>
+cudaError_t start_ring(int W, const NormArgs& a, cudaStream_t st) {
+  return W == 4 ? start_ring<T, 4, LAYER>(a, st) : W == 8 ? start_ring<T, 8, LAYER>(a, st)
+       : W == 16 ? start_ring<T, 16, LAYER>(a, st) : start_ring<T, 32, LAYER>(a, st);
+}
+
+template <typename T, int W, bool LAYER>
+cudaError_t start_ring_grad(const NormGradArgs& a, cudaStream_t st) {
+  const size_t smem = (size_t)grad_depth(W) * 3 * kRingNV * 32 * W * 16;
+  const cudaError_t e = allow_smem(ring_norm_grad_kernel<T, W, LAYER>, smem);
+  return e != cudaSuccess ? e : launch_pdl(ring_norm_grad_kernel<T, W, LAYER>, dim3(ring_grad_grid(W)), dim3(32 * W),
+                                           smem, st, a);
+}
+template <typename T, bool LAYER>
+cudaError_t start_ring_grad(int W, const NormGradArgs& a, cudaStream_t st) {
+  return W == 4 ? start_ring_grad<T, 4, LAYER>(a, st) : W == 8 ? start_ring_grad<T, 8, LAYER>(a, st)
+       : W == 16 ? start_ring_grad<T, 16, LAYER>(a, st) : start_ring_grad<T, 32, LAYER>(a, st);
 }
 
 // F(T, W, NV, VECTOR, LAYER) for the shape; one- and two-vector rows take one warp.
@@ -423,7 +659,9 @@ using namespace moe;
   if (s.W == 4) return F<T, 4, 4, VEC, LAY>(__VA_ARGS__);            \
   if (s.W == 8) return F<T, 8, 4, VEC, LAY>(__VA_ARGS__);            \
   if (s.W == 16) return F<T, 16, 4, VEC, LAY>(__VA_ARGS__);          \
-  if (s.W == 32) return F<T, 32, 4, VEC, LAY>(__VA_ARGS__);
+  if constexpr (sizeof(T) == 4) {                                    \
+    if (s.W == 32) return F<T, 32, 4, VEC, LAY>(__VA_ARGS__);        \
+  }
 
 extern "C" moe_status moe_layer_norm(const void* x, int32_t dtype, int64_t n_rows, int32_t d, int32_t kind,
                                      const float* gamma, const float* beta, float eps, void* out, float* mean,
@@ -441,8 +679,12 @@ extern "C" moe_status moe_layer_norm(const void* x, int32_t dtype, int64_t n_row
   const bool layer = kind == MOE_NORM_LAYER;
   const bool vector = d % (dtype == MOE_DTYPE_F32 ? 4 : 8) == 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == MOE_DTYPE_F32 ? MOE_NORM_PICK(start_norm, float, a, s, st)
-                                               : MOE_NORM_PICK(start_norm, bf16, a, s, st);
+  const int W = ring_warps(n_rows, d, dtype);
+  cudaError_t e;
+  if (W && dtype == MOE_DTYPE_F32) e = layer ? start_ring<float, true>(W, a, st) : start_ring<float, false>(W, a, st);
+  else if (W) e = layer ? start_ring<bf16, true>(W, a, st) : start_ring<bf16, false>(W, a, st);
+  else if (dtype == MOE_DTYPE_F32) e = MOE_NORM_PICK(start_norm, float, a, s, st);
+  else e = MOE_NORM_PICK(start_norm, bf16, a, s, st);
   return e != cudaSuccess ? fail(MOE_ERR_CUDA, "norm launch: %s", cudaGetErrorString(e)) : MOE_OK;
 }
 
@@ -452,7 +694,8 @@ extern "C" moe_status moe_layer_norm_backward_workspace_size(int64_t n_rows, int
   size_t parts = 0;
   for (int dtype : {MOE_DTYPE_F32, MOE_DTYPE_BF16}) {
     const NormShape s = norm_shape(d, dtype, kNormGradVecs);
-    const size_t p = (size_t)norm_grad_grid(s, n_rows) * s.slots;
+    const int W = ring_warps(n_rows, d, dtype);
+    const size_t p = W ? (size_t)ring_grad_grid(W) : (size_t)norm_grad_grid(s, n_rows) * s.slots;
     parts = p > parts ? p : parts;
   }
   *bytes = kAlign + align_up(parts * 2 * d * 4);
@@ -466,7 +709,9 @@ extern "C" moe_status moe_layer_norm_backward_workspace_size(int64_t n_rows, int
   if (s.W == 8) return F<T, 8, 2, VEC, LAY>(__VA_ARGS__);                     \
   if (s.W == 16) return F<T, 16, 2, VEC, LAY>(__VA_ARGS__);                   \
   if (s.W == 32 && s.NV <= 2) return F<T, 32, 2, VEC, LAY>(__VA_ARGS__);      \
-  if (s.W == 32) return F<T, 32, 4, VEC, LAY>(__VA_ARGS__);
+  if constexpr (sizeof(T) == 4) {                                             \
+    if (s.W == 32) return F<T, 32, 4, VEC, LAY>(__VA_ARGS__);                 \
+  }
 
 extern "C" moe_status moe_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_t n_rows, int32_t d,
                                               int32_t kind, const float* gamma, const float* mean, const float* rstd,
@@ -486,14 +731,19 @@ extern "C" moe_status moe_layer_norm_backward(const void* dy, const void* x, int
   if (kind == MOE_NORM_LAYER && !mean) return fail(MOE_ERR_INVALID_ARG, "mean is NULL");
   MOE_CHECK(check_ws(ws, ws_bytes, need));
   const NormShape s = norm_shape(d, dtype, kNormGradVecs);
-  const int grid = norm_grad_grid(s, n_rows);
+  const int W = ring_warps(n_rows, d, dtype);
+  const int grid = W ? ring_grad_grid(W) : norm_grad_grid(s, n_rows);
+  const int parts = W ? grid : grid * s.slots;
   float* part = at<float>(ws, kAlign);
   NormGradArgs a{dy, x, dres, gamma, mean, rstd, dx, part, n_rows, d, dgamma || dbeta};
   const bool layer = kind == MOE_NORM_LAYER;
   const bool vector = d % (dtype == MOE_DTYPE_F32 ? 4 : 8) == 0;
-  cudaError_t e = dtype == MOE_DTYPE_F32 ? MOE_NORM_PICK(start_norm_grad, float, a, s, grid, st)
-                                         : MOE_NORM_PICK(start_norm_grad, bf16, a, s, grid, st);
+  cudaError_t e;
+  if (W && dtype == MOE_DTYPE_F32) e = layer ? start_ring_grad<float, true>(W, a, st) : start_ring_grad<float, false>(W, a, st);
+  else if (W) e = layer ? start_ring_grad<bf16, true>(W, a, st) : start_ring_grad<bf16, false>(W, a, st);
+  else if (dtype == MOE_DTYPE_F32) e = MOE_NORM_PICK(start_norm_grad, float, a, s, grid, st);
+  else e = MOE_NORM_PICK(start_norm_grad, bf16, a, s, grid, st);
   if (e == cudaSuccess && (dgamma || dbeta))
-    e = launch_pdl(norm_grad_sum_kernel, dim3((d + 31) / 32, 2), dim3(256), 0, st, part, grid * s.slots, d, dgamma, dbeta);
+    e = launch_pdl(norm_grad_sum_kernel, dim3((d + 31) / 32, 2), dim3(1024), 0, st, part, parts, d, dgamma, dbeta);
   return e != cudaSuccess ? fail(MOE_ERR_CUDA, "norm backward launch: %s", cudaGetErrorString(e)) : MOE_OK;
 }
