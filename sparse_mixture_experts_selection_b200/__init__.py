@@ -135,10 +135,18 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_current_stream = None
+
+
 def _stream(stream) -> Optional[int]:
+    global _current_stream
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            import torch
+            # the handle alone: making a Stream object takes as long as a launch
+            raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+            _current_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+        return _current_stream()
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -310,42 +318,64 @@ def moe_clear_device_error(ws, stream=None) -> None:
 # ---------------------------------------------------------------------------
 # around and inside a sublayer x + dropout(MoE(norm(x)))
 # ---------------------------------------------------------------------------
-# types that are taken, by torch's names (torch is imported with the first call)
-_F32, _I32S, _BF16S = ("float32",), ("int32",), ("bfloat16",)
-_CODES, _RNG, _BYTES = ("uint8", "float8_e4m3fn"), ("int64", "uint64"), ("uint8",)
+class _Types:
+    """The types that a tensor may have, by torch's names (torch is imported with
+    the first call)."""
+    __slots__ = ("names", "dtypes")
+
+    def __init__(self, *names):
+        self.names, self.dtypes = names, None
+
+    def load(self):
+        import torch
+        self.dtypes = tuple(getattr(torch, k) for k in self.names)
+        return self.dtypes
+
+
+_F32, _I32S, _BF16S = _Types("float32"), _Types("int32"), _Types("bfloat16")
+_CODES, _RNG, _BYTES = _Types("uint8", "float8_e4m3fn"), _Types("int64", "uint64"), _Types("uint8")
 _ACT = {DTYPE_F32: _F32, DTYPE_BF16: _BF16S}
+_UNKNOWN = _Types("bool")          # an unknown dtype code: the library would refuse it too
 _torch = None
-_types = {(): ()}                  # names -> torch dtypes; no names: an unknown dtype code, nothing matches
 
 
-def _call(fn, stream, checks, *args) -> None:
-    """Check the tensors of a call -- (name, tensor, type names, number of values)
-    -- and make it on their device.  The kernels take dense arrays by pointer, so a
-    strided view, another type, a short tensor or one of another device is
-    refused here.  None and plain addresses pass."""
+def _refuse(name, t, types, n):
+    if t.dtype not in types.dtypes:
+        raise MoeError(1, f"{name} has type {t.dtype}, not {' or '.join(types.names)}")
+    if not t.is_contiguous():
+        raise MoeError(1, f"{name} is not contiguous")
+    raise MoeError(1, f"{name} has {t.numel()} values, {n} are needed")
+
+
+def _pointers(*checks):
+    """The addresses of a call's tensors and the device they are on, after a check
+    of each (name, tensor, types, number of values).  The kernels take dense
+    arrays by pointer, so a strided view, another type, a short tensor or one of
+    another device is refused here.  None and plain addresses pass."""
+    out, device, other = [], None, None
+    for name, t, types, n in checks:
+        if t is None or t.__class__ is int:
+            out.append(t)
+            continue
+        if t.dtype not in (types.dtypes or types.load()) or not t.is_contiguous() or t.numel() < n:
+            _refuse(name, t, types, n)
+        at = t.get_device()
+        if at != device:
+            if device is not None:
+                other = name
+            device = at
+        out.append(t.data_ptr())
+    if other is not None or (device is not None and device < 0):
+        raise MoeError(1, "the tensors are not on one GPU" + (f" ({other} is on another device)" if other else ""))
+    out.append(device)
+    return out
+
+
+def _enqueue(fn, device, stream, *args) -> None:
+    """Make the call on the tensors' device and stream."""
     global _torch
     if _torch is None:
         import torch as _torch
-    device = other = None
-    for name, t, names, n in checks:
-        if t is None or t.__class__ is int:
-            continue
-        types = _types.get(names)
-        if types is None:
-            types = _types[names] = tuple(getattr(_torch, k) for k in names)
-        if t.dtype not in types:
-            raise MoeError(1, f"{name} has type {t.dtype}, not {' or '.join(names)}")
-        if not t.is_contiguous():
-            raise MoeError(1, f"{name} is not contiguous")
-        if t.numel() < n:
-            raise MoeError(1, f"{name} has {t.numel()} values, {n} are needed")
-        at = t.get_device()
-        if device is None:
-            device = at
-        elif at != device:
-            other = name
-    if other is not None or (device is not None and device < 0):
-        raise MoeError(1, "the tensors are not on one GPU" + (f" ({other} is on another device)" if other else ""))
     if device is None or device == _torch.cuda.current_device():
         status = fn(*args, _stream(stream))
     else:
@@ -363,12 +393,13 @@ def moe_layer_norm(x, dtype: int, n_rows: int, d: int, kind: int, gamma, beta, e
                    codes=None, scales=None, stream=None):
     """Norm of n_rows rows of d values (NORM_LAYER or NORM_RMS); with codes and
     scales the output once more in e4m3 tiles of 1 x 128 (see include/moe.h)."""
-    n, act = n_rows * d, _ACT.get(dtype, ())
-    _call(lib().moe_layer_norm, stream, (("x", x, act, n), ("gamma", gamma, _F32, d), ("beta", beta, _F32, d),
-          ("out", out, act, n), ("mean", mean, _F32, n_rows), ("rstd", rstd, _F32, n_rows),
-          ("codes", codes, _CODES, n), ("scales", scales, _F32, n_rows * _blocks(d))),
-          _ptr(x), int(dtype), int(n_rows), int(d), int(kind), _ptr(gamma), _ptr(beta), float(eps), _ptr(out),
-          _ptr(mean), _ptr(rstd), _ptr(codes), _ptr(scales))
+    n, act = n_rows * d, _ACT.get(dtype, _UNKNOWN)
+    (p_x, p_gamma, p_beta, p_out, p_mean, p_rstd, p_codes, p_scales, device) = _pointers(
+        ("x", x, act, n), ("gamma", gamma, _F32, d), ("beta", beta, _F32, d), ("out", out, act, n),
+        ("mean", mean, _F32, n_rows), ("rstd", rstd, _F32, n_rows), ("codes", codes, _CODES, n),
+        ("scales", scales, _F32, n_rows * _blocks(d)))
+    _enqueue(lib().moe_layer_norm, device, stream, p_x, dtype, n_rows, d, kind, p_gamma, p_beta, eps, p_out, p_mean,
+             p_rstd, p_codes, p_scales)
 
 
 def moe_layer_norm_backward_workspace_size(n_rows: int, d: int) -> int:
@@ -380,43 +411,47 @@ def moe_layer_norm_backward_workspace_size(n_rows: int, d: int) -> int:
 def moe_layer_norm_backward(dy, x, dtype: int, n_rows: int, d: int, kind: int, gamma, mean, rstd, dres, dx, dgamma,
                             dbeta, ws, stream=None):
     """Gradients of moe_layer_norm; dres is added to dx (see include/moe.h)."""
-    n, act = n_rows * d, _ACT.get(dtype, ())
-    _call(lib().moe_layer_norm_backward, stream, (("dy", dy, act, n), ("x", x, act, n), ("gamma", gamma, _F32, d),
-          ("mean", mean, _F32, n_rows), ("rstd", rstd, _F32, n_rows), ("dres", dres, act, n), ("dx", dx, act, n),
-          ("dgamma", dgamma, _F32, d), ("dbeta", dbeta, _F32, d), ("ws", ws, _BYTES, 0)),
-          _ptr(dy), _ptr(x), int(dtype), int(n_rows), int(d), int(kind), _ptr(gamma), _ptr(mean), _ptr(rstd),
-          _ptr(dres), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(ws), ws.numel())
+    n, act = n_rows * d, _ACT.get(dtype, _UNKNOWN)
+    (p_dy, p_x, p_gamma, p_mean, p_rstd, p_dres, p_dx, p_dgamma, p_dbeta, p_ws, device) = _pointers(
+        ("dy", dy, act, n), ("x", x, act, n), ("gamma", gamma, _F32, d), ("mean", mean, _F32, n_rows),
+        ("rstd", rstd, _F32, n_rows), ("dres", dres, act, n), ("dx", dx, act, n), ("dgamma", dgamma, _F32, d),
+        ("dbeta", dbeta, _F32, d), ("ws", ws, _BYTES, 0))
+    _enqueue(lib().moe_layer_norm_backward, device, stream, p_dy, p_x, dtype, n_rows, d, kind, p_gamma, p_mean,
+             p_rstd, p_dres, p_dx, p_dgamma, p_dbeta, p_ws, ws.numel())
 
 
 def moe_dropout_add(x, res, dtype: int, n: int, p: float, rng, out, stream=None):
     """out = res + dropout(x) over n values; rng: int64 [2] on the device, the
     seed and the number of this draw (see include/moe.h)."""
-    act = _ACT.get(dtype, ())
-    _call(lib().moe_dropout_add, stream, (("x", x, act, n), ("res", res, act, n), ("rng", rng, _RNG, 2),
-          ("out", out, act, n)),
-          _ptr(x), _ptr(res), int(dtype), int(n), float(p), _ptr(rng), _ptr(out))
+    act = _ACT.get(dtype, _UNKNOWN)
+    (p_x, p_res, p_rng, p_out, device) = _pointers(
+        ("x", x, act, n), ("res", res, act, n), ("rng", rng, _RNG, 2), ("out", out, act, n))
+    _enqueue(lib().moe_dropout_add, device, stream, p_x, p_res, dtype, n, p, p_rng, p_out)
 
 
 def moe_dropout_backward(dy, dtype: int, n: int, p: float, rng, dx, stream=None):
     """dx = dy through the mask that moe_dropout_add drew with the same rng, p and n."""
-    act = _ACT.get(dtype, ())
-    _call(lib().moe_dropout_backward, stream, (("dy", dy, act, n), ("rng", rng, _RNG, 2), ("dx", dx, act, n)),
-          _ptr(dy), int(dtype), int(n), float(p), _ptr(rng), _ptr(dx))
+    act = _ACT.get(dtype, _UNKNOWN)
+    (p_dy, p_rng, p_dx, device) = _pointers(
+        ("dy", dy, act, n), ("rng", rng, _RNG, 2), ("dx", dx, act, n))
+    _enqueue(lib().moe_dropout_backward, device, stream, p_dy, dtype, n, p, p_rng, p_dx)
 
 
 def moe_quantize_tiles(src, src_dtype: int, n_rows: int, cols: int, codes, scales, stream=None):
     """e4m3 codes and one power-of-two scale for each 1 x 128 tile of the rows."""
-    _call(lib().moe_quantize_tiles, stream, (("src", src, _ACT.get(src_dtype, ()), n_rows * cols),
-          ("codes", codes, _CODES, n_rows * cols), ("scales", scales, _F32, n_rows * _blocks(cols))),
-          _ptr(src), int(src_dtype), int(n_rows), int(cols), _ptr(codes), _ptr(scales))
+    (p_src, p_codes, p_scales, device) = _pointers(
+        ("src", src, _ACT.get(src_dtype, _UNKNOWN), n_rows * cols), ("codes", codes, _CODES, n_rows * cols),
+        ("scales", scales, _F32, n_rows * _blocks(cols)))
+    _enqueue(lib().moe_quantize_tiles, device, stream, p_src, src_dtype, n_rows, cols, p_codes, p_scales)
 
 
 def moe_quantize_blocks(src, src_dtype: int, n_mats: int, rows: int, cols: int, codes, scales, stream=None):
     """e4m3 codes and one power-of-two scale for each 128 x 128 block of the matrices."""
     n = n_mats * rows * cols
-    _call(lib().moe_quantize_blocks, stream, (("src", src, _ACT.get(src_dtype, ()), n),
-          ("codes", codes, _CODES, n), ("scales", scales, _F32, n_mats * _blocks(rows) * _blocks(cols))),
-          _ptr(src), int(src_dtype), int(n_mats), int(rows), int(cols), _ptr(codes), _ptr(scales))
+    (p_src, p_codes, p_scales, device) = _pointers(
+        ("src", src, _ACT.get(src_dtype, _UNKNOWN), n), ("codes", codes, _CODES, n),
+        ("scales", scales, _F32, n_mats * _blocks(rows) * _blocks(cols)))
+    _enqueue(lib().moe_quantize_blocks, device, stream, p_src, src_dtype, n_mats, rows, cols, p_codes, p_scales)
 
 
 def moe_block_matmul_workspace_size(n_groups: int, n_cols: int, k: int, max_rows: int) -> int:
@@ -429,13 +464,14 @@ def moe_block_matmul(n_groups: int, n_cols: int, k: int, max_rows: int, offsets,
                      out_dtype: int, out, ws, stream=None):
     """Grouped product of block-scaled e4m3 operands (see include/moe.h); offsets
     None with one group takes all max_rows rows."""
-    _call(lib().moe_block_matmul, stream, (("offsets", offsets, _I32S, n_groups + 1), ("x", x, _CODES, max_rows * k),
-          ("x_scale", x_scale, _F32, max_rows * _blocks(k)), ("w", w, _CODES, n_groups * n_cols * k),
-          ("w_scale", w_scale, _F32, n_groups * _blocks(n_cols) * _blocks(k)),
-          ("row_scale", row_scale, _F32, max_rows), ("out", out, _ACT.get(out_dtype, ()), max_rows * n_cols),
-          ("ws", ws, _BYTES, 0)),
-          int(n_groups), int(n_cols), int(k), int(max_rows), _ptr(offsets), _ptr(x), _ptr(x_scale), _ptr(w),
-          _ptr(w_scale), _ptr(row_scale), int(out_dtype), _ptr(out), _ptr(ws), ws.numel())
+    (p_offsets, p_x, p_x_scale, p_w, p_w_scale, p_row_scale, p_out, p_ws, device) = _pointers(
+        ("offsets", offsets, _I32S, n_groups + 1), ("x", x, _CODES, max_rows * k),
+        ("x_scale", x_scale, _F32, max_rows * _blocks(k)), ("w", w, _CODES, n_groups * n_cols * k),
+        ("w_scale", w_scale, _F32, n_groups * _blocks(n_cols) * _blocks(k)),
+        ("row_scale", row_scale, _F32, max_rows), ("out", out, _ACT.get(out_dtype, _UNKNOWN), max_rows * n_cols),
+        ("ws", ws, _BYTES, 0))
+    _enqueue(lib().moe_block_matmul, device, stream, n_groups, n_cols, k, max_rows, p_offsets, p_x, p_x_scale, p_w,
+             p_w_scale, p_row_scale, out_dtype, p_out, p_ws, ws.numel())
 
 
 def moe_block_ffn_workspace_size(n_experts: int, d_model: int, d_ffn: int, max_rows: int) -> int:
@@ -450,12 +486,12 @@ def moe_block_ffn(n_experts: int, d_model: int, d_ffn: int, max_rows: int, offse
     """Grouped SwiGLU experts on block-scaled e4m3 weights (see include/moe.h)."""
     n = n_experts * d_model * d_ffn
     nb = n_experts * _blocks(d_model) * _blocks(d_ffn)
-    _call(lib().moe_block_ffn, stream, (("offsets", offsets, _I32S, n_experts + 1),
-          ("x", x, _CODES, max_rows * d_model), ("x_scale", x_scale, _F32, max_rows * _blocks(d_model)),
-          ("w_gate", w_gate, _CODES, n), ("s_gate", s_gate, _F32, nb), ("w_up", w_up, _CODES, n),
-          ("s_up", s_up, _F32, nb), ("w_down", w_down, _CODES, n), ("s_down", s_down, _F32, nb),
-          ("row_scale", row_scale, _F32, max_rows), ("out", out, _ACT.get(out_dtype, ()), max_rows * d_model),
-          ("ws", ws, _BYTES, 0)),
-          int(n_experts), int(d_model), int(d_ffn), int(max_rows), _ptr(offsets), _ptr(x), _ptr(x_scale),
-          _ptr(w_gate), _ptr(s_gate), _ptr(w_up), _ptr(s_up), _ptr(w_down), _ptr(s_down), _ptr(row_scale),
-          int(out_dtype), _ptr(out), _ptr(ws), ws.numel())
+    (p_offsets, p_x, p_x_scale, p_w_gate, p_s_gate, p_w_up, p_s_up, p_w_down, p_s_down, p_row_scale, p_out, p_ws,
+     device) = _pointers(
+        ("offsets", offsets, _I32S, n_experts + 1), ("x", x, _CODES, max_rows * d_model),
+        ("x_scale", x_scale, _F32, max_rows * _blocks(d_model)), ("w_gate", w_gate, _CODES, n),
+        ("s_gate", s_gate, _F32, nb), ("w_up", w_up, _CODES, n), ("s_up", s_up, _F32, nb),
+        ("w_down", w_down, _CODES, n), ("s_down", s_down, _F32, nb), ("row_scale", row_scale, _F32, max_rows),
+        ("out", out, _ACT.get(out_dtype, _UNKNOWN), max_rows * d_model), ("ws", ws, _BYTES, 0))
+    _enqueue(lib().moe_block_ffn, device, stream, n_experts, d_model, d_ffn, max_rows, p_offsets, p_x, p_x_scale,
+             p_w_gate, p_s_gate, p_w_up, p_s_up, p_w_down, p_s_down, p_row_scale, out_dtype, p_out, p_ws, ws.numel())

@@ -22,6 +22,15 @@
 // two of the four 128-column slots of tensor memory instead of always two, so up to four blocks are
 // on their way: a block waits about 1000 cycles on its barriers, twice its products.
 //
+// Groups of many rows run on clusters of two CTAs (cta_group::2) in units of 256 rows:
+// each CTA holds its half of the rows and half of the weight rows, so a block takes 32 KB of
+// its shared memory instead of 48.  One CTA's 128 x 256 x 128 is bound by reading its
+// operands there (about 900 cycles, of 512 of products): 8 experts x 1024 rows, 4096 x 14336,
+// 632 us on single CTAs, 589 on pairs.  A pair has the longer way from one block to
+// the next, over both CTAs' barriers (about 1800 cycles for the two blocks that tensor memory
+// holds): 256 experts x 128 rows take 3.1 ms on single CTAs, 3.5 on pairs, and
+// 512 rows over 150 experts 1.05 against 1.7 ms.
+//
 // Few rows leave few units: the blocks of the reduction are then cut into ranges,
 // each unit of a range leaves its accumulators in the workspace, and the last
 // unit of a tile to finish adds the ranges in ascending order (so the sum
@@ -48,9 +57,14 @@ namespace {
 constexpr int kBlock = 128;              // values per scale; also the k-block of a pipeline stage
 constexpr int kMaxGroups = 1024;
 constexpr int BM = 128, BN = 256;                   // rows and weight rows of a unit
-constexpr int A_BYTES = BM * kBlock, W_BYTES = kBlock * kBlock, B_BYTES = 2 * W_BYTES;
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES;      // 48 KB
-constexpr int STAGES = 4;
+constexpr int STAGE_RING = 192 * 1024;              // operands on their way
+constexpr int A_BYTES = BM * kBlock;
+// one CTA loads both blocks of 128 weight rows, a CTA of a pair 64 rows of each
+template <bool PAIR> constexpr int w_box() { return PAIR ? kBlock / 2 : kBlock; }
+template <bool PAIR> constexpr int w_bytes() { return w_box<PAIR>() * kBlock; }
+template <bool PAIR> constexpr int stages() { return STAGE_RING / (A_BYTES + 2 * w_bytes<PAIR>()); }   // 4, 6
+constexpr int MAX_STAGES = 6;
+constexpr int kPairRows = 512;                      // rows per group from which pairs run
 constexpr int SUB_ROWS = 32;                        // row box of short row tiles
 constexpr int kSwapRows = 32;                       // row tiles of at most this many rows run transposed
 constexpr int SLOTS = 4, SLOT_COLS = 128;           // tensor memory
@@ -72,7 +86,7 @@ constexpr int PART_FLOATS = 128 * 32 * EPI_WARPS;   // accumulators of a unit
 struct Control {
   float xs[2][CHUNK][BM];                           // scales of the rows, two chunks
   float ws[2][2][CHUNK];                            // and of the two blocks of weight rows
-  uint64_t full[STAGES], done[STAGES], slot_empty[SLOTS], sc_full[2], sc_empty[2], drain;
+  uint64_t full[MAX_STAGES], done[MAX_STAGES], slot_empty[SLOTS], sc_full[2], sc_empty[2], drain;
   uint32_t tmem;
   int abort, last, total;
   int warp_sum[NUM_THREADS / 32];
@@ -80,13 +94,13 @@ struct Control {
   int prefix[kMaxGroups + 1];                       // units of the groups before
   alignas(16) uint8_t piece[EPI_WARPS][32 * 64];    // a warp's 32 rows x 64 bytes on their way out
 };
-constexpr size_t SMEM_BYTES = (size_t)STAGES * STAGE_BYTES + sizeof(Control) + 1024;
+constexpr size_t SMEM_BYTES = (size_t)STAGE_RING + sizeof(Control) + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 
 int blocks_of(int n) { return (n + kBlock - 1) / kBlock; }
 
 struct BlockArgs {
-  CUtensorMap x, x32, w0, w1;       // rows in boxes of 128 and 32; weights in boxes of 128 (gate, up)
+  CUtensorMap x, x32, w0, w1;       // rows in boxes of 128 and 32; weights in boxes of 128, or 64 for a pair (gate, up)
   int G, N, K, max_rows;
   int KB, NB, NT;                   // blocks of the reduction and of the columns; column tiles
   int ranges, per;                  // ranges of the reduction, blocks per range
@@ -100,14 +114,16 @@ struct BlockArgs {
 };
 
 struct Unit {
-  int g, nt, r0, rows;              // rows: of this tile
+  int g, nt, r0, rows;              // first row and rows of this CTA
+  int rows_all;                     // rows of the tile: those of both CTAs of a pair
   int kb0, nk, range, tile;
   int n16;                          // transposed: rows rounded up to 16, else 0
   bool two;                         // both blocks of weight rows have columns
 };
 
-template <bool SWIGLU>
-__device__ __forceinline__ Unit decode(const BlockArgs& a, const int* prefix, int u) {
+template <bool SWIGLU, bool PAIR>
+__device__ __forceinline__ Unit decode(const BlockArgs& a, const int* prefix, int u, int rank) {
+  constexpr int ROWS = PAIR ? 2 * BM : BM;
   int lo = 0, hi = a.G;             // prefix[lo] <= u < prefix[lo + 1]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -117,15 +133,21 @@ __device__ __forceinline__ Unit decode(const BlockArgs& a, const int* prefix, in
   w.g = lo;
   const int r0 = a.offsets ? __ldg(a.offsets + lo) : 0;
   const int r1 = a.offsets ? __ldg(a.offsets + lo + 1) : a.max_rows;
-  const int mts = (r1 - r0 + BM - 1) / BM;
+  const int mts = (r1 - r0 + ROWS - 1) / ROWS;
   w.tile = u / a.ranges;            // every group's units are whole tiles of `ranges` units
   int local = u - prefix[lo];
   w.range = local % a.ranges;
   local /= a.ranges;
   w.nt = local / mts;
-  w.r0 = r0 + local % mts * BM;
-  w.rows = min(BM, r1 - w.r0);
-  w.n16 = w.rows <= kSwapRows ? (w.rows + 15) & ~15 : 0;
+  w.r0 = r0 + local % mts * ROWS;
+  w.rows = w.rows_all = min(ROWS, r1 - w.r0);
+  if constexpr (PAIR) {
+    // the CTAs share the rows in halves of whole warps
+    const int half = min(w.rows, (w.rows + 63) / 64 * 32);
+    w.r0 += rank ? half : 0;
+    w.rows = rank ? w.rows - half : half;
+  }
+  w.n16 = !PAIR && w.rows <= kSwapRows ? (w.rows + 15) & ~15 : 0;
   w.two = SWIGLU || w.nt * BN + kBlock < a.N;
   w.kb0 = w.range * a.per;
   w.nk = min(a.KB, w.kb0 + a.per) - w.kb0;
@@ -135,7 +157,9 @@ __device__ __forceinline__ Unit decode(const BlockArgs& a, const int* prefix, in
 // Units before each group (prefix[G] = all) from the offsets.  Offsets out of order
 // or out of range set the error word and leave no units: the tiles of ascending
 // offsets are at most those that the launch and the workspace were sized for.
+template <bool PAIR>
 __device__ __forceinline__ void scan_groups(const BlockArgs& a, Control* c) {
+  constexpr int ROWS = PAIR ? 2 * BM : BM;
   const int t = threadIdx.x, warp = t / kWarp, lane = t % kWarp;
   constexpr int PER = (kMaxGroups + NUM_THREADS - 1) / NUM_THREADS;
   int n[PER], sum = 0, bad = 0;
@@ -146,7 +170,7 @@ __device__ __forceinline__ void scan_groups(const BlockArgs& a, Control* c) {
     if (g < a.G) {
       const int r0 = a.offsets ? __ldg(a.offsets + g) : 0, r1 = a.offsets ? __ldg(a.offsets + g + 1) : a.max_rows;
       if (r0 < 0 || r1 < r0 || r1 > a.max_rows) bad = 1;
-      else n[i] = (r1 - r0 + BM - 1) / BM * a.NT * a.ranges;
+      else n[i] = (r1 - r0 + ROWS - 1) / ROWS * a.NT * a.ranges;
     }
     sum += n[i];
   }
@@ -177,7 +201,13 @@ __device__ __forceinline__ void scan_groups(const BlockArgs& a, Control* c) {
 
 // mbar_wait of common.cuh with the clock read only after many tries: these waits
 // come several times per block of 128.
-__device__ __forceinline__ bool block_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+// In a pair the other CTA is told to give up too.  What passes between the CTAs is
+// tensor memory and the loads' bytes, which order themselves: the barriers are read and, by
+// the accumulator warps, arrived on at CTA scope (an acquire or release at
+// cluster scope in every block took three times the time).
+template <bool PAIR>
+__device__ __forceinline__ bool block_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err,
+                                           uint32_t peer_abort) {
   uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -188,6 +218,7 @@ __device__ __forceinline__ bool block_wait(uint64_t* bar, uint32_t parity, volat
       if (now - t0 > kWaitLimitNs) {
         set_device_error(err, MOE_DEVERR_WAIT_TIMEOUT);
         *abort = 1;
+        if constexpr (PAIR) st_remote_u32(peer_abort, 1u);
         return false;
       }
     }
@@ -210,8 +241,9 @@ struct SlotWalk {
   }
 };
 
+// Arrive on a barrier of this CTA or, by its cluster address, of the even one.
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // Wait without giving up on *abort (drains what is in flight before the CTA
@@ -220,6 +252,19 @@ __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity, int* 
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(bar, parity))
     if (global_timer_ns() - t0 > kWaitLimitNs) { set_device_error(err, MOE_DEVERR_WAIT_TIMEOUT); return; }
+}
+
+// D (+)= A * B^T, e4m3: over one CTA's operands, or over both CTAs' halves (issued by the even one).
+template <bool PAIR>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+  else
+    tc_mma_e4m3(d, a, b, idesc, acc);
 }
 
 // One lane of the (whole) warp.
@@ -422,39 +467,54 @@ __device__ __forceinline__ void store_swiglu_columns(const BlockArgs& a, float (
   asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");   // the maxima are rewritten by the next unit
 }
 
-template <bool SWIGLU>
+template <bool SWIGLU, bool PAIR>
 __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __grid_constant__ BlockArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* sA = smem;
+  constexpr int STAGES = stages<PAIR>(), W_BYTES = w_bytes<PAIR>(), B_BYTES = 2 * W_BYTES, CTAS = PAIR ? 2 : 1;
   uint8_t* sB = smem + STAGES * A_BYTES;
-  Control* c = reinterpret_cast<Control*>(smem + STAGES * STAGE_BYTES);
+  Control* c = reinterpret_cast<Control*>(smem + STAGE_RING);
   volatile int* abort_flag = &c->abort;
   int* err = a.ctrl;
   // the same in all lanes, and known to be: the roles' loops then run on the uniform path
   const int warp = __shfl_sync(kFull, (int)threadIdx.x / kWarp, 0), lane = threadIdx.x % kWarp;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return block_wait(bar, parity, abort_flag, err); };
+  const uint32_t rank = PAIR ? cluster_rank() : 0u;
+  const uint32_t peer_abort = PAIR ? cluster_addr(&c->abort, rank ^ 1u) : 0u;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return block_wait<PAIR>(bar, parity, abort_flag, err, peer_abort); };
+  // barriers that both CTAs signal are the even one's
+  auto even = [&](uint64_t* bar) { return PAIR ? cluster_addr(bar, 0) : smem_u32(bar); };
+  auto commit = [&](uint64_t* bar) {
+    if constexpr (PAIR) tc_commit_pair(bar); else tc_commit(bar);
+  };
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) { mbar_init(&c->full[s], 1); mbar_init(&c->done[s], 1); }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&c->sc_full[b], 2 * kWarp); mbar_init(&c->sc_empty[b], EPI_WARPS);
     }
-    for (int b = 0; b < SLOTS; ++b) mbar_init(&c->slot_empty[b], EPI_WARPS);
+    for (int b = 0; b < SLOTS; ++b) mbar_init(&c->slot_empty[b], CTAS * EPI_WARPS);
     mbar_init(&c->drain, 1);
     c->abort = 0;
     fence_barrier_init();
   }
   if (warp == 1 && lane == 0) { prefetch_tmap(&a.x); prefetch_tmap(&a.x32); prefetch_tmap(&a.w0); prefetch_tmap(&a.w1); }
   __syncthreads();
-  if (warp == 0) tmem_alloc(&c->tmem, TMEM_COLS);
+  if constexpr (PAIR) {
+    __syncthreads();
+    cluster_sync_all();        // both CTAs' barriers are initialised before either signals the other
+    if (warp == 0) tmem_alloc_pair(&c->tmem, TMEM_COLS);
+  } else if (warp == 0) {
+    tmem_alloc(&c->tmem, TMEM_COLS);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   pdl_wait();
   pdl_trigger();
   const uint32_t tmem = c->tmem;
-  scan_groups(a, c);
+  scan_groups<PAIR>(a, c);
   const int total = c->prefix[a.G];
+  const int first = (int)blockIdx.x / CTAS, step = (int)gridDim.x / CTAS;
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FEW_REGS));
@@ -463,23 +523,31 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-        const Unit w = decode<SWIGLU>(a, c->prefix, u);
+      for (int u = first; u < total && ok; u += step) {
+        const Unit w = decode<SWIGLU, PAIR>(a, c->prefix, u, rank);
         const int sub = (w.rows + SUB_ROWS - 1) / SUB_ROWS;       // four boxes of 32 rows are one of 128
-        const uint32_t tx = (uint32_t)(sub * SUB_ROWS * kBlock + (w.two ? 2 : 1) * W_BYTES);
-        const int by = w.g * a.N + w.nt * (SWIGLU ? kBlock : BN);
+        const int other = PAIR ? (w.rows_all - w.rows + SUB_ROWS - 1) / SUB_ROWS : 0;
+        const uint32_t tx = (uint32_t)((sub + other) * SUB_ROWS * kBlock + CTAS * (w.two ? 2 : 1) * W_BYTES);
+        // a pair's CTAs: 64 gate and the same 64 up rows each, or each half of the tile's columns
+        const int by = w.g * a.N + w.nt * (SWIGLU ? kBlock : BN) +
+                       (PAIR ? (int)rank * (SWIGLU || !w.two ? kBlock / 2 : kBlock) : 0);
+        const int by1 = SWIGLU ? by : by + w_box<PAIR>();
         for (int i = 0; i < w.nk; ++i) {
           if (!wait(&c->done[stage], phase ^ 1u)) { ok = false; break; }
           const int k = (w.kb0 + i) * kBlock;
-          mbar_arrive_expect_tx(&c->full[stage], tx);
+          if (rank == 0) mbar_arrive_expect_tx(&c->full[stage], tx);
+          const uint32_t bar = even(&c->full[stage]);
+          auto load = [&](uint8_t* to, const CUtensorMap* map, int y) {
+            if constexpr (PAIR) tma_load_2d_pair(to, map, bar, k, y);
+            else tma_load_2d(to, map, &c->full[stage], k, y);
+          };
           // the weights first: they come from HBM, the rows mostly from L2
-          tma_load_2d(sB + stage * B_BYTES, &a.w0, &c->full[stage], k, by);
-          if (w.two) tma_load_2d(sB + stage * B_BYTES + W_BYTES, &a.w1, &c->full[stage], k, SWIGLU ? by : by + kBlock);
+          load(sB + stage * B_BYTES, &a.w0, by);
+          if (w.two) load(sB + stage * B_BYTES + W_BYTES, &a.w1, by1);
           if (sub == BM / SUB_ROWS) {
-            tma_load_2d(sA + stage * A_BYTES, &a.x, &c->full[stage], k, w.r0);
+            load(sA + stage * A_BYTES, &a.x, w.r0);
           } else {
-            for (int q = 0; q < sub; ++q)
-              tma_load_2d(sA + stage * A_BYTES + q * SUB_ROWS * kBlock, &a.x32, &c->full[stage], k, w.r0 + q * SUB_ROWS);
+            for (int q = 0; q < sub; ++q) load(sA + stage * A_BYTES + q * SUB_ROWS * kBlock, &a.x32, w.r0 + q * SUB_ROWS);
           }
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
@@ -490,17 +558,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
         ok = wait(&c->done[stage], phase ^ 1u);
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
-    } else if (warp == 1) {
-      // ---------------- MMA issuer ----------------
+    } else if (warp == 1 && rank == 0) {
+      // ---------------- MMA issuer (of a pair: the even CTA) ----------------
       const uint64_t descA = sdesc_kmajor_sw128(smem_u32(sA)), descB = sdesc_kmajor_sw128(smem_u32(sB));
       int stage = 0;
       uint32_t phase = 0;
       SlotWalk walk;
       bool ok = true;
-      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-        const Unit w = decode<SWIGLU>(a, c->prefix, u);
+      for (int u = first; u < total && ok; u += step) {
+        const Unit w = decode<SWIGLU, PAIR>(a, c->prefix, u, rank);
         const uint32_t n_slots = w.n16 == 0 || w.n16 > SLOT_COLS / 2 ? 2u : 1u;
-        const uint32_t idesc = w.n16 ? idesc_e4m3_f32(BM, w.n16) : idesc_e4m3_f32(BM, w.two ? BN : kBlock);
+        const uint32_t idesc = w.n16 ? idesc_e4m3_f32(BM, w.n16) : idesc_e4m3_f32(CTAS * BM, w.two ? BN : kBlock);
         const uint32_t second = n_slots * (SLOT_COLS / 2);     // transposed: columns of the second block of weights
         for (int i = 0; i < w.nk; ++i) {
           uint32_t before;
@@ -515,22 +583,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
           if (elect_one()) {
             if (w.n16 == 0) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) tc_mma_e4m3(d, da + 2 * k, db + 2 * k, idesc, k != 0);
+              for (int k = 0; k < 4; ++k) mma<PAIR>(d, da + 2 * k, db + 2 * k, idesc, k != 0);
             } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) tc_mma_e4m3(d, db + 2 * k, da + 2 * k, idesc, k != 0);
+              for (int k = 0; k < 4; ++k) mma<PAIR>(d, db + 2 * k, da + 2 * k, idesc, k != 0);
               if (w.two) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tc_mma_e4m3(d + second, db + W_BYTES / 16 + 2 * k, da + 2 * k, idesc, k != 0);
+                for (int k = 0; k < 4; ++k) mma<PAIR>(d + second, db + W_BYTES / 16 + 2 * k, da + 2 * k, idesc, k != 0);
               }
             }
-            tc_commit(&c->done[stage]);          // the stage is read and the sums are there
+            commit(&c->done[stage]);             // the stage is read and the sums are there
           }
           __syncwarp();
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      if (elect_one()) tc_commit(&c->drain);
+      // in a pair: the accumulator warps of both CTAs have released all slots
+      if constexpr (PAIR) {
+        for (int s = 0; s < SLOTS; ++s)
+          if (ok && !wait(&c->slot_empty[s], ((walk.parity >> s) & 1u) ^ 1u)) ok = false;
+      }
+      if (elect_one()) {
+        if constexpr (PAIR) tc_commit_local(&c->drain); else tc_commit(&c->drain);
+      }
       __syncwarp();
       wait_drain(&c->drain, 0, err);
     } else if (warp >= 2) {
@@ -538,8 +613,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
       const int t = threadIdx.x - 2 * kWarp;
       uint32_t ch = 0;                     // chunks so far; buffer ch % 2
       bool ok = true;
-      for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-        const Unit w = decode<SWIGLU>(a, c->prefix, u);
+      for (int u = first; u < total && ok; u += step) {
+        const Unit w = decode<SWIGLU, PAIR>(a, c->prefix, u, rank);
         const int j0 = SWIGLU ? w.nt : 2 * w.nt, j1 = SWIGLU ? w.nt : min(j0 + 1, a.NB - 1);
         for (int c0 = 0; c0 < w.nk; c0 += CHUNK, ++ch) {
           const uint32_t b = ch & 1u;
@@ -578,14 +653,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
     const int r = quad * 32 + lane;
     const int t = threadIdx.x - EPI_THREAD0;
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-    const uint32_t release = smem_u32(&c->slot_empty[0]);           // slot s: + 8 s
+    const uint32_t release = even(&c->slot_empty[0]);               // slot s: + 8 s
     int stage = 0;
     uint32_t phase = 0, ch = 0;
     SlotWalk walk;
     bool ok = true;
-    for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-      const Unit w = decode<SWIGLU>(a, c->prefix, u);
-      const bool swap = w.n16 != 0;
+    for (int u = first; u < total && ok; u += step) {
+      const Unit w = decode<SWIGLU, PAIR>(a, c->prefix, u, rank);
+      const bool swap = !PAIR && w.n16 != 0;
       // transposed: this half's rows t0 .. t0 + n - 1 of the tile, 16 at a time
       const int t0 = half ? (w.n16 + 31) / 32 * 16 : 0;
       const int chunks = swap ? (half ? w.n16 - t0 : (w.n16 + 31) / 32 * 16) / 16 : 0;
@@ -619,7 +694,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
           free_slots();
         } else if (!swap) {
           // the thread's row, 128 columns: a block of the plain product, or 64 gate and their 64 up columns
-          const uint32_t base = d + (uint32_t)(half * (SWIGLU ? 64 : 128));
+          const uint32_t base = d + (uint32_t)(half * (SWIGLU && !PAIR ? 64 : 128));
           const float s_first = x * (SWIGLU || half == 0 ? w0 : w1), s_last = SWIGLU ? x * w1 : s_first;
           // 16 columns arrive while the 16 before are added
           uint32_t v[2][16];
@@ -627,7 +702,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             tmem_wait16(v[q & 1]);
-            if (q < 7) tmem_ld16(base + 16 * (q + 1) + (SWIGLU && q + 1 >= 4 ? 64 : 0), v[(q + 1) & 1]);
+            if (q < 7) tmem_ld16(base + 16 * (q + 1) + (SWIGLU && !PAIR && q + 1 >= 4 ? 64 : 0), v[(q + 1) & 1]);
             else free_slots();
             const float sc = q < 4 ? s_first : s_last;
 #pragma unroll
@@ -665,9 +740,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
         }
       }
       // the barriers below want every warp: if a wait gave up in one, all leave here
-      if (SWIGLU || a.ranges > 1) ok = all_agree(ok);
+      if (SWIGLU || (!PAIR && a.ranges > 1)) ok = all_agree(ok);
       if (!ok) break;
-      if (a.ranges > 1) {
+      if (!PAIR && a.ranges > 1) {
         // leave the accumulators; the last range of the tile to arrive adds them in order
         const bool mine = !idle && (swap || r < w.rows);
         const size_t tile = (size_t)w.tile * a.ranges;
@@ -692,16 +767,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
         asm volatile("bar.sync 5, 256;" ::: "memory");
         if (!last) continue;
         if (mine) {
+          // eight ranges of the same four values in flight: few rows have few values to wait for
+          const float4* p = reinterpret_cast<const float4*>(a.part + tile * PART_FLOATS) + t;
 #pragma unroll
-          for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
-          for (int q = 0; q < a.ranges; ++q) {
-            const float4* p = reinterpret_cast<const float4*>(a.part + (tile + q) * PART_FLOATS);
+          for (int j = 0; j < 32; ++j) {
+            if (swap && 4 * j % 64 >= n) continue;
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+            for (int q0 = 0; q0 < a.ranges; q0 += 8) {
+              float4 v[8];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (swap && 4 * j % 64 >= n) continue;
-              const float4 v = __ldcg(p + j * 256 + t);
-              acc[4 * j] += v.x; acc[4 * j + 1] += v.y; acc[4 * j + 2] += v.z; acc[4 * j + 3] += v.w;
+              for (int q = 0; q < 8; ++q)
+                v[q] = q0 + q < a.ranges ? __ldcg(p + (size_t)(q0 + q) * (PART_FLOATS / 4) + j * 256)
+                                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) { sum.x += v[q].x; sum.y += v[q].y; sum.z += v[q].z; sum.w += v[q].w; }
             }
+            acc[4 * j] = sum.x; acc[4 * j + 1] = sum.y; acc[4 * j + 2] = sum.z; acc[4 * j + 3] = sum.w;
           }
         }
       }
@@ -735,8 +817,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();      // neither CTA leaves while the other may still signal it
   tc_fence_after();
-  if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
+  if (warp == 0) {
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, TMEM_COLS); else tmem_dealloc(tmem, TMEM_COLS);
+  }
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -769,6 +854,7 @@ bool tensor_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, 
 // any offsets; when they leave more than half of the SMs idle the blocks of
 // the reduction are cut into ranges, at least two blocks each.
 struct Cut {
+  bool pair;
   int nt, ranges, per;
   int64_t tiles;
 };
@@ -778,6 +864,15 @@ Cut cut_of(int n_groups, int n_cols, int k, int max_rows, bool swiglu) {
   Cut c{};
   const int kb = blocks_of(k);
   c.nt = swiglu ? blocks_of(n_cols) : (n_cols + BN - 1) / BN;
+  // pairs: groups of many rows, and tiles for two rounds of them at least
+  const int64_t pair_tiles = ((int64_t)max_rows / (2 * BM) + std::min(n_groups, max_rows)) * c.nt;
+  c.pair = max_rows >= (int64_t)kPairRows * n_groups && pair_tiles >= kSms;
+  if (c.pair) {
+    c.tiles = pair_tiles;
+    c.per = kb;
+    c.ranges = 1;
+    return c;
+  }
   c.tiles = ((int64_t)max_rows / BM + std::min(n_groups, max_rows)) * c.nt;
   const int64_t want = c.tiles > 0 ? kSms / c.tiles : 1;
   c.per = kb;
@@ -800,8 +895,9 @@ cudaError_t product(int G, int N, int K, int max_rows, const int* offsets, const
   const Cut cut = cut_of(G, N, K, max_rows, swiglu);
   BlockArgs a{};
   const void* w1 = swiglu ? o.w1 : o.w0;
+  const uint32_t box = cut.pair ? w_box<true>() : w_box<false>();
   if (!tensor_map(&a.x, o.x, max_rows, K, BM) || !tensor_map(&a.x32, o.x, max_rows, K, SUB_ROWS) ||
-      !tensor_map(&a.w0, o.w0, (uint64_t)G * N, K, kBlock) || !tensor_map(&a.w1, w1, (uint64_t)G * N, K, kBlock))
+      !tensor_map(&a.w0, o.w0, (uint64_t)G * N, K, box) || !tensor_map(&a.w1, w1, (uint64_t)G * N, K, box))
     return cudaErrorInvalidValue;
   a.G = G; a.N = N; a.K = K; a.max_rows = max_rows;
   a.KB = blocks_of(K); a.NB = blocks_of(N); a.NT = cut.nt;
@@ -814,15 +910,33 @@ cudaError_t product(int G, int N, int K, int max_rows, const int* offsets, const
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (dev >= 64 || !attr_done[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(block_product_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(block_product_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
-    if (e != cudaSuccess) return e;
+    for (auto kern : {block_product_kernel<true, true>, block_product_kernel<true, false>,
+                      block_product_kernel<false, true>, block_product_kernel<false, false>}) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+      if (e != cudaSuccess) return e;
+    }
     if (dev < 64) attr_done[dev] = true;
   }
-  const unsigned grid = (unsigned)std::min<int64_t>(cut.tiles * cut.ranges, std::max(sms, 1));
-  return launch_pdl(swiglu ? block_product_kernel<true> : block_product_kernel<false>, dim3(grid), dim3(NUM_THREADS),
-                    SMEM_BYTES, st, a);
+  if (!cut.pair) {
+    const unsigned grid = (unsigned)std::min<int64_t>(cut.tiles * cut.ranges, std::max(sms, 1));
+    return launch_pdl(swiglu ? block_product_kernel<true, false> : block_product_kernel<false, false>, dim3(grid),
+                      dim3(NUM_THREADS), SMEM_BYTES, st, a);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (unsigned)std::min<int64_t>(cut.tiles, std::max(sms / 2, 1)));
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kUsePdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, swiglu ? block_product_kernel<true, true> : block_product_kernel<false, true>, a);
 }
 
 moe_status check_product(int n_groups, int n_cols, int k, int max_rows) {

@@ -309,6 +309,8 @@ MATMULS = [  # rows of each group, n, k
     ([1], 1, 16), ([1], 128, 128), ([3, 0, 5], 130, 144), ([128], 256, 256), ([129, 0, 0, 1], 257, 272),
     ([300, 17], 255, 640), ([0, 40, 0], 96, 16), ([64] * 20, 64, 384), ([1] * 70, 33, 400), ([513], 1000, 112),
     ([31, 33, 95, 97, 127, 128, 255, 257], 384, 1024), ([0, 0], 64, 64), ([7], 2048, 7168), ([2, 1], 320, 4112),
+    # enough rows a group and tiles for CTA pairs: whole, ragged and odd, one block of columns in the last tile
+    ([2048], 4400, 384), ([1500, 29, 700], 6301, 272), ([0, 3000, 1], 4952, 912),
 ]
 
 
@@ -375,6 +377,7 @@ def test_block_matmul_reports_bad_offsets(offsets):
 FFNS = [  # rows of each expert, d, f
     ([1], 16, 16), ([1], 256, 128), ([5, 0, 130], 144, 208), ([64, 1, 0, 33], 512, 384), ([257], 128, 1040),
     ([3] * 40, 272, 96), ([1], 2048, 640), ([0, 200, 129], 640, 272),
+    ([3001, 1100], 2320, 1168),                     # both products on CTA pairs
 ]
 
 
