@@ -423,8 +423,8 @@ moe_status moe_layer_norm(const void* x, int32_t dtype, int64_t n_rows, int32_t 
  *   (the residual branch), added before the one rounding.
  *   dx [n_rows, d] (dtype; may be dy or dres itself); dgamma, dbeta [d] float32
  *   out, either may be NULL.  n_rows = 0 writes zeros to dgamma and dbeta.
- *   ws: at least moe_layer_norm_backward_workspace_size bytes, its first 256
- *   zeroed once (see moe_workspace_size).  The sums over rows run in a fixed
+ *   ws: at least moe_layer_norm_backward_workspace_size bytes (its first 256
+ *   bytes are not used by this call).  The sums over rows run in a fixed
  *   order; one workspace serves calls whose work does not overlap on the GPU.
  */
 moe_status moe_layer_norm_backward_workspace_size(int64_t n_rows, int32_t d, size_t* bytes);
@@ -445,7 +445,8 @@ moe_status moe_layer_norm_backward(const void* dy, const void* x, int32_t dtype,
  *   rng [2] uint64 on the DEVICE: the generator's seed and the number of this
  *   draw (8-byte aligned).  It is read when the kernel runs, so a captured graph draws anew
  *   once the caller changes it; no two draws may share (rng[0], rng[1]).
- *   x, res, out [n] (dtype); res may be NULL for 0; out may be x or res itself.
+ *   x, res, out [n] (dtype); res may be NULL for 0; out may be x or res itself
+ *   (dx may be dy).
  *   0 <= p <= 1; p = 1 keeps nothing.  Dropped values are not read into the
  *   result: an infinity or NaN there leaves out_i = res_i.
  */
@@ -466,7 +467,7 @@ moe_status moe_dropout_backward(const void* dy, int32_t dtype, int64_t n, double
  * separate arrays, as such checkpoints store them.  Values must be finite; a NaN
  * becomes the code of NaN.
  *   src [n_rows, cols] or [n_mats, rows, cols] (src_dtype), 16-byte aligned;
- *   cols a positive multiple of 16; codes 16-byte aligned, same shape as src;
+ *   cols a positive multiple of 16; rows, cols at most 2^30; codes 16-byte aligned, same shape as src;
  *   scales [n_rows, ceil(cols/128)], or [n_mats, ceil(rows/128), ceil(cols/128)].
  */
 moe_status moe_quantize_tiles(const void* src, int32_t src_dtype, int64_t n_rows, int32_t cols,
@@ -485,7 +486,11 @@ moe_status moe_quantize_blocks(const void* src, int32_t src_dtype, int32_t n_mat
  *   offsets[n_groups] <= max_rows; or NULL with n_groups = 1 for all max_rows rows.
  *   x [max_rows, k], x_scale [max_rows, ceil(k/128)];  w [n_groups, n_cols, k],
  *   w_scale [n_groups, ceil(n_cols/128), ceil(k/128)];  row_scale [max_rows] float32
- *   or NULL for 1.  k a positive multiple of 16; n_cols >= 1; n_groups <= 1024.
+ *   or NULL for 1.  k a positive multiple of 16; n_cols >= 1; n_groups <= 1024;
+ *   k, n_cols <= 2^20.  out must not overlap an input.
+ *   Groups of at least 512 rows on average run on CTA pairs (256-row tiles), row
+ *   tiles of at most 32 rows with the weights as the tensor core's first operand:
+ *   the same sums, with the tensor core's own order inside 32 products.
  *   out [max_rows, n_cols], out_dtype MOE_DTYPE_BF16 or MOE_DTYPE_F32.  Rows
  *   outside [offsets[0], offsets[n_groups]) are left as they were.
  *   ws: its first 256 bytes zeroed once, and again after an error; offsets out

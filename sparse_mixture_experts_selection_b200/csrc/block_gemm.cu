@@ -15,12 +15,13 @@
 // codes and scales.  Units of a group go row tile fastest, so CTAs that run
 // together share weight tiles through L2 and weights stream from HBM about once.
 //
-// A row tile of more than kSwapRows rows is the M = 128 operand and the weights are
-// N = 256.  A shorter one runs transposed: each block of weights is an M = 128 operand, the
-// rows rounded up to 16 are N.  The tensor cores, the loads and the accumulators then
-// do n / 128 of a tile's work instead of padding the rows, and a block takes one or
-// two of the four 128-column slots of tensor memory instead of always two, so up to four blocks are
-// on their way: a block waits about 1000 cycles on its barriers, twice its products.
+// A row tile of more than kSwapRows = 32 rows is the M = 128 operand and the weights
+// are N = 256: a block takes two of the four slots of 128 columns of tensor memory.  A shorter
+// tile runs transposed, each block of weights an M = 128 operand and the rows,
+// rounded up to 16, N: one slot, so four blocks are on their way, and no padding
+// rows in the epilogue (150 experts of a few rows: 1.05 against 1.12 ms, one row:
+// 22 against 38 us).  Tiles of up to 64 rows are no faster that way (64 experts of 64
+// rows: 65 against 58 us): the weights still pass shared memory whole.
 //
 // Groups of many rows run on clusters of two CTAs (cta_group::2) in units of 256 rows:
 // each CTA holds its half of the rows and half of the weight rows, so a block takes 32 KB of
@@ -68,6 +69,8 @@ constexpr int kPairRows = 512;                      // rows per group from which
 constexpr int SUB_ROWS = 32;                        // row box of short row tiles
 constexpr int kSwapRows = 32;                       // row tiles of at most this many rows run transposed
 constexpr int SLOTS = 4, SLOT_COLS = 128;           // tensor memory
+constexpr int SECOND = SLOT_COLS / 2;               // transposed: columns of the second block of weights in its slot
+static_assert(kSwapRows == 32, "a transposed tile's rows: 16 to each half of the accumulator warps");
 constexpr int EPI_WARPS = 8;
 constexpr int NUM_THREADS = 128 + 32 * EPI_WARPS;
 constexpr int EPI_THREAD0 = 128;
@@ -418,41 +421,39 @@ __device__ __forceinline__ void store_swiglu(const BlockArgs& a, float (&acc)[12
   if (half == 0) a.out_scale[row * a.NB + w.nt] = pow2(e);
 }
 
-// Transposed tiles: the thread holds columns col (acc[t]) and col + 128 (acc[64 + t])
-// of rows row0 + t, t < n; a warp writes 32 neighbouring columns of a row at a time.
+// Transposed tiles: the thread holds columns col (acc[t]) and col + 128 (acc[16 + t])
+// of rows row0 + t, t < n <= 16; a warp writes 32 neighbouring columns of a row at a time.
 template <typename T>
 __device__ __forceinline__ void store_columns(const BlockArgs& a, const float (&acc)[128], int row0, int n, int col) {
   const int lane = threadIdx.x % kWarp;
-  // lane t holds the scales of rows t and t + 32
-  const float rs0 = a.row_scale && lane < n ? __ldg(a.row_scale + row0 + lane) : 1.0f;
-  const float rs1 = a.row_scale && lane + 32 < n ? __ldg(a.row_scale + row0 + lane + 32) : 1.0f;
+  const float rs_lane = a.row_scale && lane < n ? __ldg(a.row_scale + row0 + lane) : 1.0f;    // of row `lane`
   T* out = static_cast<T*>(a.out) + (size_t)row0 * a.N + col;
 #pragma unroll
-  for (int t = 0; t < 64; ++t) {
+  for (int t = 0; t < 16; ++t) {
     if (t >= n) break;
-    const float rs = __shfl_sync(kFull, t < 32 ? rs0 : rs1, t % 32);
+    const float rs = __shfl_sync(kFull, rs_lane, t);
     if (col < a.N) out[(size_t)t * a.N] = from_f32<T>(acc[t] * rs);
-    if (col + kBlock < a.N) out[(size_t)t * a.N + kBlock] = from_f32<T>(acc[64 + t] * rs);
+    if (col + kBlock < a.N) out[(size_t)t * a.N + kBlock] = from_f32<T>(acc[16 + t] * rs);
   }
 }
 
-// Transposed SwiGLU: acc[t] is the gate and acc[64 + t] the up value of column col
+// Transposed SwiGLU: acc[t] is the gate and acc[16 + t] the up value of column col
 // of row row0 + t; the tile's 128 columns are the 128 lanes of the four warps
 // of this half of the rows, which share their maxima through shared memory.
 __device__ __forceinline__ void store_swiglu_columns(const BlockArgs& a, float (&acc)[128], const Unit& w, int row0,
                                                      int t0, int n, int r, int half, Control* c) {
   const int col = w.nt * kBlock + r, quad = r / 32;
 #pragma unroll
-  for (int t = 0; t < 64; ++t) {
+  for (int t = 0; t < 16; ++t) {
     if (t >= n) break;
-    acc[t] = col < a.N ? silu(acc[t]) * acc[64 + t] : 0.0f;
+    acc[t] = col < a.N ? silu(acc[t]) * acc[16 + t] : 0.0f;
     // magnitudes order like their bits; a NaN does not count
     const uint32_t top = __reduce_max_sync(kFull, acc[t] == acc[t] ? __float_as_uint(fabsf(acc[t])) : 0u);
     if (r % 32 == 0) c->top[quad][t0 + t] = __uint_as_float(top);
   }
   asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
 #pragma unroll
-  for (int t = 0; t < 64; ++t) {
+  for (int t = 0; t < 16; ++t) {
     if (t >= n) break;
     float top = 0.0f;
 #pragma unroll
@@ -567,9 +568,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
       bool ok = true;
       for (int u = first; u < total && ok; u += step) {
         const Unit w = decode<SWIGLU, PAIR>(a, c->prefix, u, rank);
-        const uint32_t n_slots = w.n16 == 0 || w.n16 > SLOT_COLS / 2 ? 2u : 1u;
+        const uint32_t n_slots = w.n16 == 0 ? 2u : 1u;
         const uint32_t idesc = w.n16 ? idesc_e4m3_f32(BM, w.n16) : idesc_e4m3_f32(CTAS * BM, w.two ? BN : kBlock);
-        const uint32_t second = n_slots * (SLOT_COLS / 2);     // transposed: columns of the second block of weights
         for (int i = 0; i < w.nk; ++i) {
           uint32_t before;
           const uint32_t s = walk.take(n_slots, before);
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
               for (int k = 0; k < 4; ++k) mma<PAIR>(d, db + 2 * k, da + 2 * k, idesc, k != 0);
               if (w.two) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma<PAIR>(d + second, db + W_BYTES / 16 + 2 * k, da + 2 * k, idesc, k != 0);
+                for (int k = 0; k < 4; ++k) mma<PAIR>(d + SECOND, db + W_BYTES / 16 + 2 * k, da + 2 * k, idesc, k != 0);
               }
             }
             commit(&c->done[stage]);             // the stage is read and the sums are there
@@ -661,14 +661,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
     for (int u = first; u < total && ok; u += step) {
       const Unit w = decode<SWIGLU, PAIR>(a, c->prefix, u, rank);
       const bool swap = !PAIR && w.n16 != 0;
-      // transposed: this half's rows t0 .. t0 + n - 1 of the tile, 16 at a time
-      const int t0 = half ? (w.n16 + 31) / 32 * 16 : 0;
-      const int chunks = swap ? (half ? w.n16 - t0 : (w.n16 + 31) / 32 * 16) / 16 : 0;
-      const int n = swap ? max(0, min(w.rows - t0, 16 * chunks)) : 0;
-      const uint32_t n_slots = !swap || w.n16 > SLOT_COLS / 2 ? 2u : 1u;
-      const uint32_t second = n_slots * (SLOT_COLS / 2);
+      // transposed: this half's rows t0 .. t0 + n - 1 of the tile
+      const int t0 = 16 * half, n = swap ? max(0, min(16, w.rows - t0)) : 0;
+      const uint32_t n_slots = swap ? 1u : 2u;
       // warps without rows, or without columns, only keep the slots moving
-      const bool idle = swap ? chunks == 0 : quad * 32 >= w.rows || (half == 1 && !w.two);
+      const bool idle = swap ? n == 0 : quad * 32 >= w.rows || (half == 1 && !w.two);
       float acc[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
@@ -710,27 +707,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
               fma2(acc[16 * q + j], acc[16 * q + j + 1], __uint_as_float(v[q & 1][j]), __uint_as_float(v[q & 1][j + 1]), sc);
           }
         } else {
-          // one column of each block of weights, 16 rows at a time
+          // one column of each block of weights, 16 rows: acc[t] and acc[16 + t]
           const float* xs = &c->xs[sb][i % CHUNK][t0];
+          uint32_t v0[16], v1[16];
+          tmem_ld16(d + t0, v0);
+          tmem_ld16(d + SECOND + t0, v1);
+          tmem_wait16(v0);
+          tmem_wait16(v1);
+          free_slots();
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (q < chunks) {
-              uint32_t v0[16], v1[16];
-              tmem_ld16(d + t0 + 16 * q, v0);
-              tmem_ld16(d + second + t0 + 16 * q, v1);
-              tmem_wait16(v0);
-              tmem_wait16(v1);
-              if (q == chunks - 1) free_slots();
-#pragma unroll
-              for (int j = 0; j < 16; j += 4) {
-                const float4 xv = *reinterpret_cast<const float4*>(xs + 16 * q + j);
-                const int p = 16 * q + j;
-                fma2(acc[p], acc[p + 1], __uint_as_float(v0[j]), __uint_as_float(v0[j + 1]), xv.x * w0, xv.y * w0);
-                fma2(acc[p + 2], acc[p + 3], __uint_as_float(v0[j + 2]), __uint_as_float(v0[j + 3]), xv.z * w0, xv.w * w0);
-                fma2(acc[64 + p], acc[65 + p], __uint_as_float(v1[j]), __uint_as_float(v1[j + 1]), xv.x * w1, xv.y * w1);
-                fma2(acc[66 + p], acc[67 + p], __uint_as_float(v1[j + 2]), __uint_as_float(v1[j + 3]), xv.z * w1, xv.w * w1);
-              }
-            }
+          for (int j = 0; j < 16; j += 4) {
+            const float4 xv = *reinterpret_cast<const float4*>(xs + j);
+            fma2(acc[j], acc[j + 1], __uint_as_float(v0[j]), __uint_as_float(v0[j + 1]), xv.x * w0, xv.y * w0);
+            fma2(acc[j + 2], acc[j + 3], __uint_as_float(v0[j + 2]), __uint_as_float(v0[j + 3]), xv.z * w0, xv.w * w0);
+            fma2(acc[16 + j], acc[17 + j], __uint_as_float(v1[j]), __uint_as_float(v1[j + 1]), xv.x * w1, xv.y * w1);
+            fma2(acc[18 + j], acc[19 + j], __uint_as_float(v1[j + 2]), __uint_as_float(v1[j + 3]), xv.z * w1, xv.w * w1);
           }
         }
         if (i % CHUNK == CHUNK - 1 || i == w.nk - 1) {
@@ -750,7 +741,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
         if (mine)
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            if (!swap || 4 * j % 64 < n)
+            if (!swap || j < 8)
               __stcg(here + j * 256 + t, make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]));
         __threadfence();
         asm volatile("bar.sync 5, 256;" ::: "memory");
@@ -771,7 +762,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
           const float4* p = reinterpret_cast<const float4*>(a.part + tile * PART_FLOATS) + t;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            if (swap && 4 * j % 64 >= n) continue;
+            if (swap && j >= 8) continue;
             float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
             for (int q0 = 0; q0 < a.ranges; q0 += 8) {

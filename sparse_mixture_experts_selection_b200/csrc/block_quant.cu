@@ -39,7 +39,9 @@ __device__ __forceinline__ void store8(uint8_t* p, const float (&v)[8], float in
 }
 
 // Half a warp per tile, eight values per lane: one 16-byte load (bf16) and one
-// 8-byte store of codes a lane, no shared memory.  Bound by memory.
+// 8-byte store of codes a lane, no shared memory; kTiles tiles a time, their loads in
+// flight together.  Bound by memory.
+constexpr int kTiles = 4;
 template <typename TIn>
 __global__ void __launch_bounds__(256) quantize_tiles_kernel(const TIn* __restrict__ src, int64_t n_tiles, int tiles,
                                                              int cols, uint8_t* __restrict__ codes,
@@ -47,22 +49,39 @@ __global__ void __launch_bounds__(256) quantize_tiles_kernel(const TIn* __restri
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x % 16;
-  // whole warps walk together: their shuffles name all lanes
+  // whole warps walk together, two tiles each time: their shuffles name all lanes
   const int64_t step = (int64_t)gridDim.x * (blockDim.x / 16);
-  for (int64_t t0 = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) / 32 * 2; t0 < n_tiles; t0 += step) {
-    const int64_t t = t0 + threadIdx.x / 16 % 2;
-    const int64_t r = t / tiles;
-    const int c = (int)(t - r * tiles) * 128 + lane * 8;
-    const bool valid = t < n_tiles && c < cols;
-    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (valid) load8(src + r * cols + c, v);
-    float top = top8(v);
+  int64_t t0 = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) / 32 * 2;
+  // row and tile in the row, carried along: a 64-bit division a tile would take longer than its memory
+  int64_t row = (t0 + threadIdx.x / 16 % 2) / tiles;
+  int in_row = (int)((t0 + threadIdx.x / 16 % 2) - row * tiles);
+  const int64_t rows_step = step / tiles;
+  const int tiles_step = (int)(step - rows_step * tiles);
+  for (; t0 < n_tiles; t0 += kTiles * step) {
+    float v[kTiles][8];
+    int64_t at[kTiles];                              // -1: no values there
 #pragma unroll
-    for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
-    const int e = e4m3_scale_exponent(top);
-    if (valid) {
-      store8(codes + r * cols + c, v, pow2(-e));
-      if (lane == 0) scales[t] = pow2(e);
+    for (int k = 0; k < kTiles; ++k) {
+      const int64_t t = t0 + k * step + threadIdx.x / 16 % 2;
+      const int c = in_row * 128 + lane * 8;
+      at[k] = t < n_tiles && c < cols ? row * cols + c : -1;
+      row += rows_step;
+      in_row += tiles_step;
+      if (in_row >= tiles) { in_row -= tiles; ++row; }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
+      if (at[k] >= 0) load8(src + at[k], v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kTiles; ++k) {
+      float top = top8(v[k]);
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+      const int e = e4m3_scale_exponent(top);
+      if (at[k] >= 0) {
+        store8(codes + at[k], v[k], pow2(-e));
+        if (lane == 0) scales[t0 + k * step + threadIdx.x / 16 % 2] = pow2(e);
+      }
     }
   }
 }
@@ -105,9 +124,12 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const TIn* __restr
   if (threadIdx.x == 0) scales[b] = pow2(e);
 }
 
+constexpr int kMaxSide = 1 << 30;        // rounding up to blocks stays within 32 bits
+
 moe_status check_source(const void* src, int dtype, int cols, const void* codes, const void* scales, bool empty) {
   if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16) return fail(MOE_ERR_INVALID_ARG, "src_dtype=%d", dtype);
   if (cols < 16 || cols % 16) return fail(MOE_ERR_INVALID_ARG, "cols=%d must be a positive multiple of 16", cols);
+  if (cols > kMaxSide) return fail(MOE_ERR_UNSUPPORTED, "cols=%d > 2^30", cols);
   if (empty) return MOE_OK;
   MOE_NONNULL(src); MOE_NONNULL(codes); MOE_NONNULL4(scales);
   return MOE_OK;
@@ -145,6 +167,7 @@ extern "C" moe_status moe_quantize_tiles(const void* src, int32_t src_dtype, int
 extern "C" moe_status moe_quantize_blocks(const void* src, int32_t src_dtype, int32_t n_mats, int32_t rows,
                                           int32_t cols, uint8_t* codes, float* scales, void* stream) {
   if (n_mats < 0 || rows < 0) return fail(MOE_ERR_INVALID_ARG, "n_mats=%d rows=%d", n_mats, rows);
+  if (rows > kMaxSide) return fail(MOE_ERR_UNSUPPORTED, "rows=%d > 2^30", rows);
   const bool empty = n_mats == 0 || rows == 0;
   MOE_CHECK(check_source(src, src_dtype, cols, codes, scales, empty));
   if (empty) return MOE_OK;

@@ -635,7 +635,7 @@ cudaError_t start_ring_grad(int W, const NormGradArgs& a, cudaStream_t st) {
 moe_status check_rows(int dtype, int64_t n_rows, int d, int kind) {
   if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16) return fail(MOE_ERR_INVALID_ARG, "dtype=%d", dtype);
   if (n_rows < 0) return fail(MOE_ERR_INVALID_ARG, "n_rows=%lld < 0", (long long)n_rows);
-  if (n_rows > (int64_t)1 << 31) return fail(MOE_ERR_UNSUPPORTED, "n_rows=%lld > 2^31", (long long)n_rows);
+  if (n_rows > 0x7FFFFFFF) return fail(MOE_ERR_UNSUPPORTED, "n_rows=%lld above 2^31", (long long)n_rows);
   if (d < 1) return fail(MOE_ERR_INVALID_ARG, "d=%d < 1", d);
   if (d > kMaxNormCols) return fail(MOE_ERR_UNSUPPORTED, "d=%d > %d", d, kMaxNormCols);
   if (kind != MOE_NORM_LAYER && kind != MOE_NORM_RMS) return fail(MOE_ERR_INVALID_ARG, "kind=%d", kind);

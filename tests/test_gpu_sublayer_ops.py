@@ -100,9 +100,15 @@ def test_norm_without_gains_and_in_place():
     assert torch.equal(want, same)
     y, m, r = ref.norm(x, True)
     close(host(want), y, ref.norm_bound(x, True, None, y, m, r, "bf16"))
+    # a long batch of wide rows: the rows ahead are on their way while this one is written
+    t = dev(norm_inputs(1500, 2048, "bf16", 6)[0], torch.bfloat16)
+    want, _, _, _, _ = run_norm(t, "bf16", moe.NORM_RMS, None, None)
+    same, _, _, _, _ = run_norm(t, "bf16", moe.NORM_RMS, None, None, out=t)
+    assert torch.equal(want, same)
 
 
-@pytest.mark.parametrize("shape", [(1, 16), (5, 128), (33, 144), (64, 2048), (7, 7168), (3, 16384), (300, 272)])
+@pytest.mark.parametrize("shape", [(1, 16), (5, 128), (33, 144), (64, 2048), (7, 7168), (3, 16384), (300, 272),
+                                   (700, 2048), (605, 7168), (600, 9008)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_norm_tiles_are_the_quantized_output(shape, dtype):
     n, d = shape
@@ -234,7 +240,7 @@ def test_dropout_leaves_dropped_nans_out():
 # ---------------------------------------------------------------------------
 # quantizers
 # ---------------------------------------------------------------------------
-@pytest.mark.parametrize("shape", [(1, 16), (3, 112), (5, 128), (37, 144), (300, 7168), (4097, 64)])
+@pytest.mark.parametrize("shape", [(1, 16), (3, 112), (5, 128), (37, 144), (300, 7168), (4097, 64), (5000, 1040)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_quantize_tiles_bit_exact(shape, dtype):
     n, c = shape
@@ -308,7 +314,7 @@ def check_matmul(out, v, s, w, wsc, offsets, dtype, row_scale=None):
 MATMULS = [  # rows of each group, n, k
     ([1], 1, 16), ([1], 128, 128), ([3, 0, 5], 130, 144), ([128], 256, 256), ([129, 0, 0, 1], 257, 272),
     ([300, 17], 255, 640), ([0, 40, 0], 96, 16), ([64] * 20, 64, 384), ([1] * 70, 33, 400), ([513], 1000, 112),
-    ([31, 33, 95, 97, 127, 128, 255, 257], 384, 1024), ([0, 0], 64, 64), ([7], 2048, 7168), ([2, 1], 320, 4112),
+    ([31, 33, 95, 97, 127, 128, 255, 257], 384, 1024), ([1, 0] * 512, 40, 144), ([16, 17, 32, 15, 160, 144], 513, 528), ([0, 0], 64, 64), ([7], 2048, 7168), ([2, 1], 320, 4112),
     # enough rows a group and tiles for CTA pairs: whole, ragged and odd, one block of columns in the last tile
     ([2048], 4400, 384), ([1500, 29, 700], 6301, 272), ([0, 3000, 1], 4952, 912),
 ]
@@ -461,6 +467,44 @@ def test_captured_and_replayed_with_new_inputs():
         torch.cuda.synchronize()
         assert torch.equal(out, replayed)
     assert moe.moe_get_device_error(ws) == 0
+
+
+def test_calls_in_turn_share_a_workspace():
+    """A workspace that the layer, a product cut into ranges, one that is not and the
+    experts use in turn: the counters in its control block do not meet."""
+    rng = np.random.default_rng(62)
+    w = mi.WORKLOADS["deepseek_v3"].with_(T=64, d_model=256, E_r=16, E_s=0, K=2, d_ffn=128, n_groups=1, topk_groups=1,
+                                          group_topn=0)
+    cfg = moe.config_for(w)
+    nbytes = max(moe.moe_workspace_size(cfg), moe.moe_block_matmul_workspace_size(1, 1500, 7168, 3),
+                 moe.moe_block_matmul_workspace_size(1, 1500, 7168, 2000), moe.moe_block_ffn_workspace_size(1, 2048, 256, 2))
+    ws = moe.alloc_workspace(nbytes)
+    W = [dev(mi.gen_weight(w, k), torch.bfloat16) for k in ("gate", "up", "down")]
+    h, e, y = dev(mi.gen_h(w), torch.bfloat16), dev(mi.gen_centroids(w)), filled((64, 256), torch.bfloat16)
+    v, s = operands(rng, 2000, 7168)
+    m, ms = operands(rng, 1500, 7168, 1)
+    vc, sd, mc, msd = codes_of(v), dev(s), codes_of(m), dev(ms)
+    few, many = filled((3, 1500), torch.float32), filled((2000, 1500), torch.float32)
+    F = ffn_weights(rng, 1, 2048, 256)
+    F = [(codes_of(a), dev(b)) for a, b in F]
+    xq, xs = ref.quantize_tiles(rounded(rng.normal(size=(2, 2048)), "bf16"))
+    xq, xs, out = codes_of(xq), dev(xs), filled((2, 2048), torch.float32)
+    seen = []
+    for _ in range(3):
+        for t in (few, many, out, y):
+            t.fill_(-7.0)
+        moe.moe_layer_forward(cfg, h, e, None, *W, None, None, None, y, ws)
+        moe.moe_block_matmul(1, 1500, 7168, 3, None, vc, sd, mc, msd, None, moe.DTYPE_F32, few, ws)
+        moe.moe_block_matmul(1, 1500, 7168, 2000, None, vc, sd, mc, msd, None, moe.DTYPE_F32, many, ws)
+        moe.moe_block_ffn(1, 2048, 256, 2, None, xq, xs, *F[0], *F[1], *F[2], None, moe.DTYPE_F32, out, ws)
+        moe.moe_block_matmul(1, 1500, 7168, 3, None, vc, sd, mc, msd, None, moe.DTYPE_F32, few, ws)
+        torch.cuda.synchronize()
+        assert moe.moe_get_device_error(ws) == 0
+        seen.append([t.clone() for t in (few, many, out, y)])
+    for a, b in zip(seen[0] * 2, seen[1] + seen[2]):
+        assert torch.equal(a, b)
+    check_matmul(few, v[:3], s[:3], m, ms, [0, 3], "f32")
+    check_matmul(many[:64], v[:64], s[:64], m, ms, [0, 64], "f32")
 
 
 def test_on_a_stream_of_its_own():

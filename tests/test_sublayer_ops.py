@@ -112,10 +112,11 @@ def test_quantizer_refusals():
     for n, cols, dtype, src, codes, scales, want in (
             (4, 24, BF, P, P, P, 1), (4, 0, BF, P, P, P, 1), (-1, 32, BF, P, P, P, 1), (4, 32, 2, P, P, P, 1),
             (4, 32, BF, None, P, P, 1), (4, 32, BF, P + 8, P, P, 1), (4, 32, F32, P, P + 1, P, 1),
-            (4, 32, F32, P, P, P + 2, 1), (0, 32, BF, None, None, None, 0)):
+            (4, 32, F32, P, P, P + 2, 1), (4, (1 << 30) + 16, BF, P, P, P, 2), (0, 32, BF, None, None, None, 0)):
         assert status("moe_quantize_tiles", src, dtype, n, cols, codes, scales, None) == want
         assert status("moe_quantize_blocks", src, dtype, 1, n, cols, codes, scales, None) == want
     assert status("moe_quantize_blocks", P, BF, -1, 4, 32, P, P, None) == 1
+    assert status("moe_quantize_blocks", P, BF, 1, (1 << 30) + 1, 32, P, P, None) == 2
 
 
 @pytest.mark.parametrize("change,want", [
