@@ -29,8 +29,9 @@
 // operands there (about 900 cycles, of 512 of products): 8 experts x 1024 rows, 4096 x 14336,
 // 632 us on single CTAs, 589 on pairs.  A pair has the longer way from one block to
 // the next, over both CTAs' barriers (about 1800 cycles for the two blocks that tensor memory
-// holds): 256 experts x 128 rows take 3.1 ms on single CTAs, 3.5 on pairs, and
-// 512 rows over 150 experts 1.05 against 1.7 ms.
+// holds): 256 experts x 128 rows take 3.1 ms on single CTAs, 3.5 on pairs; at 512
+// rows a group both take as long (346 and 350 us for 8 x 512 rows), at 640 a pair's third tile of
+// 256 costs more (59 against 76 us for one group, 14336 x 4096), from 768 on pairs win.
 //
 // Few rows leave few units: the blocks of the reduction are then cut into ranges,
 // each unit of a range leaves its accumulators in the workspace, and the last
@@ -65,7 +66,7 @@ template <bool PAIR> constexpr int w_box() { return PAIR ? kBlock / 2 : kBlock; 
 template <bool PAIR> constexpr int w_bytes() { return w_box<PAIR>() * kBlock; }
 template <bool PAIR> constexpr int stages() { return STAGE_RING / (A_BYTES + 2 * w_bytes<PAIR>()); }   // 4, 6
 constexpr int MAX_STAGES = 6;
-constexpr int kPairRows = 512;                      // rows per group from which pairs run
+constexpr int kPairRows = 768;                      // rows per group from which pairs run
 constexpr int SUB_ROWS = 32;                        // row box of short row tiles
 constexpr int kSwapRows = 32;                       // row tiles of at most this many rows run transposed
 constexpr int SLOTS = 4, SLOT_COLS = 128;           // tensor memory

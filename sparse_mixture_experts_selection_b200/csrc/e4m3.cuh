@@ -10,22 +10,12 @@ namespace moe {
 
 // e with 2^e the smallest power of two such that amax <= 448 * 2^e, i.e. with
 // amax = M * 2^E (1 <= M < 2): e = E - 8 + [M > 1.75]; at least -126 (a normal
-// fp32 scale); 0 for amax == 0.
+// fp32 scale, below which subnormal amax fall); 0 for amax == 0.
 __device__ __forceinline__ int e4m3_scale_exponent(float amax) {
   const uint32_t b = __float_as_uint(amax) & 0x7FFFFFFFu;
-  if (b == 0) return 0;
-  int E;
-  uint32_t mant;
-  if ((b >> 23) == 0) {                        // subnormal amax
-    const int p = 31 - __clz(b);
-    E = p - 149;
-    mant = (b << (23 - p)) & 0x7FFFFFu;
-  } else {
-    E = (int)(b >> 23) - 127;
-    mant = b & 0x7FFFFFu;
-  }
-  const int e = E - 8 + (mant > 0x600000u ? 1 : 0);
-  return e < -126 ? -126 : e;
+  // a mantissa above that of 1.75 (0x600000) carries into the exponent
+  const int e = (int)((b + 0x1FFFFFu) >> 23) - (127 + 8);
+  return b == 0 ? 0 : max(e, -126);
 }
 
 // 2^e, exact, for -126 <= e <= 127

@@ -316,7 +316,7 @@ MATMULS = [  # rows of each group, n, k
     ([300, 17], 255, 640), ([0, 40, 0], 96, 16), ([64] * 20, 64, 384), ([1] * 70, 33, 400), ([513], 1000, 112),
     ([31, 33, 95, 97, 127, 128, 255, 257], 384, 1024), ([1, 0] * 512, 40, 144), ([16, 17, 32, 15, 160, 144], 513, 528), ([0, 0], 64, 64), ([7], 2048, 7168), ([2, 1], 320, 4112),
     # enough rows a group and tiles for CTA pairs: whole, ragged and odd, one block of columns in the last tile
-    ([2048], 4400, 384), ([1500, 29, 700], 6301, 272), ([0, 3000, 1], 4952, 912),
+    ([2048], 4400, 384), ([1700, 29, 900], 6301, 272), ([0, 3000, 1], 4952, 912),
 ]
 
 
