@@ -19,19 +19,21 @@
 // are N = 256: a block takes two of the four slots of 128 columns of tensor memory.  A shorter
 // tile runs transposed, each block of weights an M = 128 operand and the rows,
 // rounded up to 16, N: one slot, so four blocks are on their way, and no padding
-// rows in the epilogue (150 experts of a few rows: 1.05 against 1.12 ms, one row:
-// 22 against 38 us).  Tiles of up to 64 rows are no faster that way (64 experts of 64
-// rows: 65 against 58 us): the weights still pass shared memory whole.
+// rows in the epilogue (2048 x 7168 weights, one row: 22 against 61 us; 150 experts of 4
+// rows: 364 against 374; 64 experts of 32 rows: 185 both).  Tiles of up to 64 rows are no faster
+// that way (64 experts of 64 rows, 1400 x 2032: 65 against 58 us): the weights still pass
+// shared memory whole.
 //
 // Groups of many rows run on clusters of two CTAs (cta_group::2) in units of 256 rows:
 // each CTA holds its half of the rows and half of the weight rows, so a block takes 32 KB of
-// its shared memory instead of 48.  One CTA's 128 x 256 x 128 is bound by reading its
-// operands there (about 900 cycles, of 512 of products): 8 experts x 1024 rows, 4096 x 14336,
-// 632 us on single CTAs, 589 on pairs.  A pair has the longer way from one block to
-// the next, over both CTAs' barriers (about 1800 cycles for the two blocks that tensor memory
-// holds): 256 experts x 128 rows take 3.1 ms on single CTAs, 3.5 on pairs; at 512
-// rows a group both take as long (346 and 350 us for 8 x 512 rows), at 640 a pair's third tile of
-// 256 costs more (59 against 76 us for one group, 14336 x 4096), from 768 on pairs win.
+// its shared memory, and of the way there from L2, instead of 48.  The tensor cores take 512
+// cycles for a block either way; a single CTA comes to about 1150 with its loads, a CTA of a pair to
+// about 1050.  14336 x 4096 weights, single CTAs against pairs: 8 groups of 1024 rows 543
+// and 485 us, of 768 rows 416 and 370, of 512 rows 287 and 257, one of 768 rows 75 and 66.  A tile of
+// 256 that is not full costs more than one of 128: one group of 640 rows 54 and 66 us, 256
+// groups of 128 rows (2048 x 7168) 684 and 940.  The launch knows the groups' sum alone, and of
+// ragged groups the last tiles are half empty: 128 rows a group with pairs, 64 without.  From 768
+// rows a group on pairs' gain of a tenth is more than that.
 //
 // Few rows leave few units: the blocks of the reduction are then cut into ranges,
 // each unit of a range leaves its accumulators in the workspace, and the last
@@ -39,12 +41,13 @@
 // does not depend on which one was last) and runs the epilogue.
 //
 // Warp roles (384 threads): warp 0 = TMA producer (+ tensor memory), warp 1 = MMA
-// issuer, warps 2 and 3 = the scales of the next blocks, turned from rows of
-// blocks into blocks of rows in shared memory (read where they lie, a warp would
-// touch 32 lines a block), warps 4 .. 11 = accumulators and epilogue: warp w reads
+// issuer, warps 4 .. 11 = accumulators and epilogue: warp w reads
 // the tensor memory lanes 32 (w % 4) .. + 31 and one half of the columns.  A
 // thread of theirs holds 128 accumulators and 32 values on their way; the first
-// four warps give up registers for that (setmaxnreg).
+// four warps (2 and 3 only fill their warpgroup) give up registers for that (setmaxnreg).
+// Each thread fetches the scales of its own row, four blocks at a time and four blocks
+// ahead, into registers.  Two warps that staged them in shared memory for all, with a barrier
+// each way, cost 8 x 1024 rows 587 us instead of 522.
 #include <algorithm>
 #include <cuda.h>
 
@@ -76,11 +79,11 @@ constexpr int EPI_WARPS = 8;
 constexpr int NUM_THREADS = 128 + 32 * EPI_WARPS;
 constexpr int EPI_THREAD0 = 128;
 // 3 x 128 threads are launched with 168 registers each: 128 x 72 + 256 x 216 are as many
-constexpr int FEW_REGS = 72, MANY_REGS = 216;
+constexpr int FEW_REGS = 40, MANY_REGS = 232;
 static_assert(128 * FEW_REGS + 32 * EPI_WARPS * MANY_REGS <= NUM_THREADS * 168, "registers of the launch");
 constexpr int TMEM_COLS = 512;
 constexpr int MAX_RANGES = 32;
-constexpr int CHUNK = 8;                            // blocks whose scales are staged together
+constexpr int CHUNK = 4;                            // blocks whose scales are fetched together
 // byte counters of the tiles whose reduction is cut, in the control block of the
 // workspace: words 20 .. 63 (word 0 is the error word, 16 and 17 are the unit
 // counters of the layer's GEMMs, which may share the workspace)
@@ -88,9 +91,8 @@ constexpr int COUNTER_WORD0 = 20, MAX_CUT_TILES = 44 * 4;
 constexpr int PART_FLOATS = 128 * 32 * EPI_WARPS;   // accumulators of a unit
 
 struct Control {
-  float xs[2][CHUNK][BM];                           // scales of the rows, two chunks
-  float ws[2][2][CHUNK];                            // and of the two blocks of weight rows
-  uint64_t full[MAX_STAGES], done[MAX_STAGES], slot_empty[SLOTS], sc_full[2], sc_empty[2], drain;
+  alignas(16) float xs[EPI_WARPS][CHUNK][kSwapRows / 2];   // transposed: scales of a warp's 16 rows
+  uint64_t full[MAX_STAGES], done[MAX_STAGES], slot_empty[SLOTS], drain;
   uint32_t tmem;
   int abort, last, total;
   int warp_sum[NUM_THREADS / 32];
@@ -110,7 +112,7 @@ struct BlockArgs {
   int ranges, per;                  // ranges of the reduction, blocks per range
   const int* offsets;
   const float *xs, *ws0, *ws1, *row_scale;
-  int out_f32;
+  int out_f32, scales16;            // scales16: scales at 16-byte addresses
   void* out;                        // plain: out; SwiGLU: the codes of A
   float* out_scale;                 // SwiGLU: the scales of A
   float* part;                      // [tiles][ranges][PART_FLOATS]
@@ -491,9 +493,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
   };
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) { mbar_init(&c->full[s], 1); mbar_init(&c->done[s], 1); }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&c->sc_full[b], 2 * kWarp); mbar_init(&c->sc_empty[b], EPI_WARPS);
-    }
     for (int b = 0; b < SLOTS; ++b) mbar_init(&c->slot_empty[b], CTAS * EPI_WARPS);
     mbar_init(&c->drain, 1);
     c->abort = 0;
@@ -609,43 +608,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
       }
       __syncwarp();
       wait_drain(&c->drain, 0, err);
-    } else if (warp >= 2) {
-      // ---------------- scales ----------------
-      const int t = threadIdx.x - 2 * kWarp;
-      uint32_t ch = 0;                     // chunks so far; buffer ch % 2
-      bool ok = true;
-      for (int u = first; u < total && ok; u += step) {
-        const Unit w = decode<SWIGLU, PAIR>(a, c->prefix, u, rank);
-        const int j0 = SWIGLU ? w.nt : 2 * w.nt, j1 = SWIGLU ? w.nt : min(j0 + 1, a.NB - 1);
-        for (int c0 = 0; c0 < w.nk; c0 += CHUNK, ++ch) {
-          const uint32_t b = ch & 1u;
-          const int n = min(CHUNK, w.nk - c0), k = w.kb0 + c0;
-          if (!wait(&c->sc_empty[b], ((ch >> 1) & 1u) ^ 1u)) { ok = false; break; }
-          for (int r = t; r < w.rows; r += 2 * kWarp) {
-            const float* p = a.xs + (size_t)(w.r0 + r) * a.KB + k;
-            if (n == CHUNK && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-              float4 v[CHUNK / 4];
-#pragma unroll
-              for (int i = 0; i < CHUNK / 4; ++i) v[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
-#pragma unroll
-              for (int i = 0; i < CHUNK / 4; ++i) {
-                c->xs[b][4 * i][r] = v[i].x; c->xs[b][4 * i + 1][r] = v[i].y;
-                c->xs[b][4 * i + 2][r] = v[i].z; c->xs[b][4 * i + 3][r] = v[i].w;
-              }
-            } else {
-              float v[CHUNK];
-#pragma unroll
-              for (int i = 0; i < CHUNK; ++i) v[i] = i < n ? __ldg(p + i) : 0.0f;
-#pragma unroll
-              for (int i = 0; i < CHUNK; ++i) c->xs[b][i][r] = v[i];
-            }
-          }
-          if (t < 2 * CHUNK && t % CHUNK < n)
-            c->ws[b][t / CHUNK][t % CHUNK] =
-                __ldg((t < CHUNK ? a.ws0 : a.ws1) + ((size_t)w.g * a.NB + (t < CHUNK ? j0 : j1)) * a.KB + k + t % CHUNK);
-          mbar_arrive(&c->sc_full[b]);
-        }
-      }
     }
   } else {
     // ---------------- accumulators and epilogue ----------------
@@ -656,7 +618,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t release = even(&c->slot_empty[0]);               // slot s: + 8 s
     int stage = 0;
-    uint32_t phase = 0, ch = 0;
+    uint32_t phase = 0;
     SlotWalk walk;
     bool ok = true;
     for (int u = first; u < total && ok; u += step) {
@@ -667,16 +629,55 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
       const uint32_t n_slots = swap ? 1u : 2u;
       // warps without rows, or without columns, only keep the slots moving
       const bool idle = swap ? n == 0 : quad * 32 >= w.rows || (half == 1 && !w.two);
+      // scales of this thread's row (transposed: of the row that it fetches for its warp) and of the
+      // weights' blocks; `vectors`: whole rows of scales are 16-byte vectors
+      const float* xp = a.xs + (size_t)(w.r0 + (swap ? min(t0 + lane % 16, w.rows - 1) : min(r, w.rows - 1))) * a.KB + w.kb0;
+      const size_t wrow = (size_t)w.g * a.NB;
+      const int j1 = SWIGLU ? w.nt : min(2 * w.nt + 1, a.NB - 1), j0 = SWIGLU ? w.nt : !swap && half ? j1 : 2 * w.nt;
+      const float *ap = a.ws0 + (wrow + j0) * a.KB + w.kb0, *bp = a.ws1 + (wrow + j1) * a.KB + w.kb0;
+      const bool vectors = !((a.KB | w.kb0) & 3) && a.scales16;
+      auto fetch = [&](float (&v)[CHUNK], const float* p, int i) {
+        if (vectors) {
+          const float4 q = __ldg(reinterpret_cast<const float4*>(p + i));
+          v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < CHUNK; ++j) v[j] = i + j < w.nk ? __ldg(p + i + j) : 0.0f;
+        }
+      };
+      float nx[CHUNK], na[CHUNK], nb[CHUNK], sa[CHUNK], sb[CHUNK];
+#pragma unroll
+      for (int j = 0; j < CHUNK; ++j) nx[j] = na[j] = nb[j] = sa[j] = sb[j] = 0.0f;
+      auto fetch_all = [&](int i) {
+        fetch(nx, xp, i);
+        fetch(na, ap, i);
+        if (SWIGLU || swap) fetch(nb, bp, i);
+      };
+      if (!idle) fetch_all(0);
       float acc[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
       for (int i = 0; i < w.nk; ++i) {
-        const uint32_t sb = ch & 1u;
         uint32_t before;
         const uint32_t s = walk.take(n_slots, before);
-        if (i % CHUNK == 0 && !__all_sync(kFull, wait(&c->sc_full[sb], (ch >> 1) & 1u))) { ok = false; break; }
-        const float w0 = c->ws[sb][0][i % CHUNK], w1 = c->ws[sb][1][i % CHUNK];
-        const float x = swap ? 0.0f : c->xs[sb][i % CHUNK][r];
+        if (!idle && i % CHUNK == 0) {
+          if (swap) {
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < CHUNK; ++j)
+              if (lane < 16) c->xs[warp - 4][j][lane] = nx[j];
+            __syncwarp();
+          }
+#pragma unroll
+          for (int j = 0; j < CHUNK; ++j) {
+            sa[j] = swap ? na[j] : nx[j] * na[j];
+            sb[j] = swap ? nb[j] : SWIGLU ? nx[j] * nb[j] : 0.0f;
+          }
+          if (i + CHUNK < w.nk) fetch_all(i + CHUNK);
+        }
+        const float w0 = sa[0], w1 = sb[0];
+#pragma unroll
+        for (int j = 0; j + 1 < CHUNK; ++j) { sa[j] = sa[j + 1]; sb[j] = sb[j + 1]; }
         if (!__all_sync(kFull, wait(&c->done[stage], phase))) { ok = false; break; }
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         tc_fence_after();
@@ -693,7 +694,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
         } else if (!swap) {
           // the thread's row, 128 columns: a block of the plain product, or 64 gate and their 64 up columns
           const uint32_t base = d + (uint32_t)(half * (SWIGLU && !PAIR ? 64 : 128));
-          const float s_first = x * (SWIGLU || half == 0 ? w0 : w1), s_last = SWIGLU ? x * w1 : s_first;
+          const float s_first = w0, s_last = SWIGLU ? w1 : w0;
           // 16 columns arrive while the 16 before are added
           uint32_t v[2][16];
           tmem_ld16(base, v[0]);
@@ -709,7 +710,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
           }
         } else {
           // one column of each block of weights, 16 rows: acc[t] and acc[16 + t]
-          const float* xs = &c->xs[sb][i % CHUNK][t0];
+          const float* xs = c->xs[warp - 4][i % CHUNK];
           uint32_t v0[16], v1[16];
           tmem_ld16(d + t0, v0);
           tmem_ld16(d + SECOND + t0, v1);
@@ -724,11 +725,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
             fma2(acc[16 + j], acc[17 + j], __uint_as_float(v1[j]), __uint_as_float(v1[j + 1]), xv.x * w1, xv.y * w1);
             fma2(acc[18 + j], acc[19 + j], __uint_as_float(v1[j + 2]), __uint_as_float(v1[j + 3]), xv.z * w1, xv.w * w1);
           }
-        }
-        if (i % CHUNK == CHUNK - 1 || i == w.nk - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&c->sc_empty[sb]);
-          ++ch;
         }
       }
       // the barriers below want every warp: if a wait gave up in one, all leave here
@@ -896,6 +892,8 @@ cudaError_t product(int G, int N, int K, int max_rows, const int* offsets, const
   a.ranges = cut.ranges; a.per = cut.per;
   a.offsets = offsets;
   a.xs = o.xs; a.ws0 = o.ws0; a.ws1 = swiglu ? o.ws1 : o.ws0; a.row_scale = o.row_scale;
+  a.scales16 = ((reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws0) |
+                 reinterpret_cast<uintptr_t>(a.ws1)) & 15) == 0;
   a.out_f32 = out_f32; a.out = out; a.out_scale = out_scale; a.part = part; a.ctrl = ctrl;
   static bool attr_done[64] = {};
   int dev = 0, sms = 0;
