@@ -350,6 +350,32 @@ def test_block_matmul_without_offsets_and_first_rows_skipped():
     assert (host(part)[:20] == -7).all() and (host(part)[111:] == -7).all()
 
 
+@pytest.mark.parametrize("rows,n,k", [([100, 7, 200], 300, 512), ([1], 200, 2048), ([2100], 4352, 1024)])
+@pytest.mark.parametrize("shifted", [(1, 0), (0, 1), (3, 2)])
+def test_block_matmul_scales_at_any_four_bytes(rows, n, k, shifted):
+    """Scales that begin between 16-byte addresses, and NaN in the words around them,
+    give the very sums that aligned ones do."""
+    rng = np.random.default_rng(57)
+    offsets = dev(np.concatenate([[0], np.cumsum(rows)]), torch.int32)
+    R, g = sum(rows), len(rows)
+    v, s = operands(rng, R, k)
+    w, wsc = operands(rng, n, k, g)
+    x, wc = codes_of(v), codes_of(w)
+    outs = []
+    for by in [(0, 0), shifted]:
+        scales = []
+        for a, b in zip([dev(s), dev(wsc)], by):
+            room = torch.full((a.numel() + 8,), float("nan"), device="cuda")
+            room[b:b + a.numel()] = a.flatten()
+            scales.append(room[b:b + a.numel()].view(a.shape))
+        out = filled((R, n), torch.float32)
+        ws = moe.alloc_workspace(moe.moe_block_matmul_workspace_size(g, n, k, R))
+        moe.moe_block_matmul(g, n, k, R, offsets, x, scales[0], wc, scales[1], None, moe.DTYPE_F32, out, ws)
+        torch.cuda.synchronize()
+        outs.append(out)
+    assert torch.equal(outs[0], outs[1]) and torch.isfinite(outs[0]).all()
+
+
 def test_block_matmul_nan_codes_stay_in_their_rows_and_columns():
     rng = np.random.default_rng(51)
     v, s = operands(rng, 140, 384)
