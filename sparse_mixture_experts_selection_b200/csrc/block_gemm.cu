@@ -38,7 +38,10 @@
 // Few rows leave few units: the blocks of the reduction are then cut into ranges,
 // each unit of a range leaves its accumulators in the workspace, and the last
 // unit of a tile to finish adds the ranges in ascending order (so the sum
-// does not depend on which one was last) and runs the epilogue.
+// does not depend on which one was last) and runs the epilogue.  That one CTA has all ranges
+// to read, 128 KB each when all rows are there, so few are better than one for every SM: 2048 x
+// 7168 weights, 64 rows: 48 us with 18 ranges, 30 with 8, 26 with 6, 32 with 4; one row: 19 us with 18,
+// 17 with 8, 19 with 6, 22 with 4.
 //
 // Warp roles (384 threads): warp 0 = TMA producer (+ tensor memory), warp 1 = MMA
 // issuer, warps 4 .. 11 = accumulators and epilogue: warp w reads
@@ -49,6 +52,7 @@
 // ahead, into registers.  Two warps that staged them in shared memory for all, with a barrier
 // each way, cost 8 x 1024 rows 587 us instead of 522.
 #include <algorithm>
+#include <type_traits>
 #include <cuda.h>
 
 #include "api.h"
@@ -82,7 +86,9 @@ constexpr int EPI_THREAD0 = 128;
 constexpr int FEW_REGS = 40, MANY_REGS = 232;
 static_assert(128 * FEW_REGS + 32 * EPI_WARPS * MANY_REGS <= NUM_THREADS * 168, "registers of the launch");
 constexpr int TMEM_COLS = 512;
-constexpr int MAX_RANGES = 32;
+// most ranges of a reduction: of launches of transposed tiles alone, and of others, whose
+// sums are longer
+constexpr int MAX_RANGES = 8, MAX_RANGES_LONG = 6;
 constexpr int CHUNK = 4;                            // blocks whose scales are fetched together
 // byte counters of the tiles whose reduction is cut, in the control block of the
 // workspace: words 20 .. 63 (word 0 is the error word, 16 and 17 are the unit
@@ -735,10 +741,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
         const bool mine = !idle && (swap || r < w.rows);
         const size_t tile = (size_t)w.tile * a.ranges;
         float4* here = reinterpret_cast<float4*>(a.part + (tile + w.range) * PART_FLOATS);
+        // fours of acc; a transposed tile's are the rows 4 j .. 4 j + 3 of both blocks of weights
+        auto used = [&](int j) { return !swap || (j < 8 && 4 * (j % 4) < n); };
         if (mine)
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            if (!swap || j < 8)
+            if (used(j))
               __stcg(here + j * 256 + t, make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]));
         __threadfence();
         asm volatile("bar.sync 5, 256;" ::: "memory");
@@ -755,23 +763,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
         asm volatile("bar.sync 5, 256;" ::: "memory");
         if (!last) continue;
         if (mine) {
-          // eight ranges of the same four values in flight: few rows have few values to wait for
           const float4* p = reinterpret_cast<const float4*>(a.part + tile * PART_FLOATS) + t;
+          // two fours of all ranges in flight
+          auto join = [&](int j, int k, auto most) {
+            constexpr int MOST = decltype(most)::value;
+            float4 v[2][MOST];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (swap && j >= 8) continue;
-            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-            for (int q0 = 0; q0 < a.ranges; q0 += 8) {
-              float4 v[8];
+            for (int q = 0; q < MOST; ++q)
 #pragma unroll
-              for (int q = 0; q < 8; ++q)
-                v[q] = q0 + q < a.ranges ? __ldcg(p + (size_t)(q0 + q) * (PART_FLOATS / 4) + j * 256)
-                                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              for (int h = 0; h < 2; ++h)
+                v[h][q] = q < a.ranges ? __ldcg(p + (size_t)q * (PART_FLOATS / 4) + (h ? k : j) * 256)
+                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-              for (int q = 0; q < 8; ++q) { sum.x += v[q].x; sum.y += v[q].y; sum.z += v[q].z; sum.w += v[q].w; }
+            for (int h = 0; h < 2; ++h) {
+              float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+              for (int q = 0; q < MOST; ++q) { sum.x += v[h][q].x; sum.y += v[h][q].y; sum.z += v[h][q].z; sum.w += v[h][q].w; }
+              float* to = acc + 4 * (h ? k : j);
+              to[0] = sum.x; to[1] = sum.y; to[2] = sum.z; to[3] = sum.w;
             }
-            acc[4 * j] = sum.x; acc[4 * j + 1] = sum.y; acc[4 * j + 2] = sum.z; acc[4 * j + 3] = sum.w;
+          };
+          if (swap) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (4 * j < n) join(j, j + 4, std::integral_constant<int, MAX_RANGES>());
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) join(j, j + 1, std::integral_constant<int, MAX_RANGES_LONG>());
           }
         }
       }
@@ -851,9 +869,10 @@ constexpr int kSms = 148;
 Cut cut_of(int n_groups, int n_cols, int k, int max_rows, bool swiglu) {
   Cut c{};
   const int kb = blocks_of(k);
+  const int64_t some = std::min(n_groups, max_rows);     // at most so many groups have rows
   c.nt = swiglu ? blocks_of(n_cols) : (n_cols + BN - 1) / BN;
   // pairs: groups of many rows, and tiles for two rounds of them at least
-  const int64_t pair_tiles = ((int64_t)max_rows / (2 * BM) + std::min(n_groups, max_rows)) * c.nt;
+  const int64_t pair_tiles = ((int64_t)max_rows + (2 * BM - 1) * some) / (2 * BM) * c.nt;
   c.pair = max_rows >= (int64_t)kPairRows * n_groups && pair_tiles >= kSms;
   if (c.pair) {
     c.tiles = pair_tiles;
@@ -861,11 +880,12 @@ Cut cut_of(int n_groups, int n_cols, int k, int max_rows, bool swiglu) {
     c.ranges = 1;
     return c;
   }
-  c.tiles = ((int64_t)max_rows / BM + std::min(n_groups, max_rows)) * c.nt;
+  c.tiles = ((int64_t)max_rows + (BM - 1) * some) / BM * c.nt;
+  const int most = max_rows <= kSwapRows ? MAX_RANGES : MAX_RANGES_LONG;
   const int64_t want = c.tiles > 0 ? kSms / c.tiles : 1;
   c.per = kb;
   if (want >= 2 && c.tiles <= MAX_CUT_TILES && kb >= 4)
-    c.per = std::max({2, (int)((kb + want - 1) / want), (kb + MAX_RANGES - 1) / MAX_RANGES});
+    c.per = std::max({2, (int)((kb + want - 1) / want), (kb + most - 1) / most});
   c.ranges = (kb + c.per - 1) / c.per;
   return c;
 }
