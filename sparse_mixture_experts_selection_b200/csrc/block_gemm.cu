@@ -24,16 +24,21 @@
 // that way (64 experts of 64 rows, 1400 x 2032: 65 against 58 us): the weights still pass
 // shared memory whole.
 //
+// What bounds a block of 128 rows is the way of its sums through the accumulator warps, not the
+// tensor cores (512 cycles) nor the loads (20 KB of the 48 left out: 536 instead of 558 us).  Of
+// about 1220 cycles on a single CTA the warps read tensor memory and add for 445, release it and
+// add the last sums for 180, prepare scales and the next wait for 120, wait for the tensor cores
+// for 175, and a unit's epilogue comes to 185 for each of its 32 blocks.
+//
 // Groups of many rows run on clusters of two CTAs (cta_group::2) in units of 256 rows:
 // each CTA holds its half of the rows and half of the weight rows, so a block takes 32 KB of
-// its shared memory, and of the way there from L2, instead of 48.  The tensor cores take 512
-// cycles for a block either way; a single CTA comes to about 1150 with its loads, a CTA of a pair to
-// about 1050.  14336 x 4096 weights, single CTAs against pairs: 8 groups of 1024 rows 543
-// and 485 us, of 768 rows 416 and 370, of 512 rows 287 and 257, one of 768 rows 75 and 66.  A tile of
-// 256 that is not full costs more than one of 128: one group of 640 rows 54 and 66 us, 256
-// groups of 128 rows (2048 x 7168) 684 and 940.  The launch knows the groups' sum alone, and of
-// ragged groups the last tiles are half empty: 128 rows a group with pairs, 64 without.  From 768
-// rows a group on pairs' gain of a tenth is more than that.
+// its shared memory, and of the way there from L2, instead of 48.
+// 14336 x 4096 weights, single CTAs against pairs: 8 groups of 1024 rows 543 and 485 us, of
+// 768 rows 416 and 370, of 512 rows 287 and 257, one of 768 rows 75 and 66.  A tile of 256 that
+// is not full costs more than one of 128: one group of 640 rows 54 and 66 us, 256 groups of 128
+// rows (2048 x 7168) 684 and 940.  The launch knows the groups' sum alone, and of ragged groups
+// the last tiles are half empty: 128 rows a group with pairs, 64 without.  From 768 rows a
+// group on pairs' gain of a tenth is more than that.
 //
 // Few rows leave few units: the blocks of the reduction are then cut into ranges,
 // each unit of a range leaves its accumulators in the workspace, and the last
