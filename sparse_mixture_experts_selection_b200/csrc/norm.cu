@@ -10,6 +10,7 @@
 // (NV 16-byte vectors per lane), so the centred sum of squares needs no second
 // read and does not cancel for rows with a large mean; sums go lane -> warp
 // (shuffles) -> row (shared memory), always in the same order.
+#include <algorithm>
 #include <cmath>
 
 #include "api.h"
@@ -23,12 +24,11 @@ namespace {
 constexpr int kMaxNormCols = 16384;
 constexpr int kSms = 148;
 constexpr int kNormGrid = 2 * kSms;      // blocks of the row-by-row backward: their partial sums are the workspace
-// Wide rows of long batches run in resident blocks that walk the rows, the next
-// kDepth rows on their way to shared memory meanwhile: see ring_norm_kernel.
+// Wide rows run in resident blocks that walk the rows, the next kDepth rows on their way
+// to shared memory meanwhile: see ring_norm_kernel.
 constexpr int kDepth = 3;
 constexpr int grad_depth(int W) { return W == 32 ? 2 : 4; }    // of the backward: 192 KB
-constexpr int kRingRows = 4 * kSms;      // fewer rows: one block per row has the shorter way
-constexpr int kRingVecs = 128;           // rows of at most this many 16-byte vectors fit one or two warps
+constexpr int kRingRows = 3 * kSms, kRingVecs = 128, kRingGradVecs = 64;     // where those run
 
 // How rows map to warps: W warps per row, NV vectors of V elements per lane,
 // `slots` rows at a time in a block of `threads`.
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W) norm_grad_kernel(const 
 }
 
 // ---------------------------------------------------------------------------
-// wide rows, long batches
+// wide rows
 // ---------------------------------------------------------------------------
 // Each thread copies its own two vectors of a row to its own place in shared
 // memory (cp.async, past the L1 cache) kDepth rows ahead, so nothing but the sums is
@@ -370,6 +370,9 @@ __global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W) norm_grad_kernel(const 
 // gains stay in registers.  One block per row instead reads the gains again with each
 // row and has no load in flight while it sums: 47 against 27 us for 4096 x 7168 bf16
 // (4.3 TB/s; a plain copy of that size takes 21 us), and depth 4 or 6 takes 31 or 33.
+// From three rows an SM on (bf16, 7168 columns, ring and block per row: 296 rows 10.2 us both, 444 rows
+// 10.2 and 12.3, 1184 rows 14.3 and 20.5) and rows of 128 16-byte vectors (8192 rows of 1024 columns
+// 16.4 and 18.5, of 512 columns 16.4 and 12.3: half of the threads have none).
 // What bounds it now is issuing: 20 instructions a value, 69 % of the slots.
 __device__ __forceinline__ void copy16(void* smem, const void* global, bool in) {
   const int bytes = in ? 16 : 0;                       // 0: zeros are written
@@ -428,7 +431,9 @@ __global__ void __launch_bounds__(32 * W, W <= 16 ? 32 / W : 1) ring_norm_kernel
 // of 512 threads on an SM: 44 us for 4096 x 7168 bf16 with dres (5.4 TB/s), and 4 for
 // the parts' sums.  The row read twice from shared memory with 1024 threads on an SM
 // took 41 instructions a value instead of 28 and 64 us, 1024 threads with one vector
-// each 73 us.
+// each 73 us.  It wins for any number of rows from 64 vectors a row on, where norm_grad_kernel
+// would need a second warp a row (bf16, this and norm_grad_kernel: 1 x 7168 11 and 17 us, 64 x 7168 13 and
+// 19, 444 x 7168 17 and 38, 512 x 512 11 and 15; with 32 vectors 8192 x 256 24 both, 32768 x 256 62 and 36).
 template <typename T, int W, bool LAYER>
 __global__ void __launch_bounds__(32 * W, W <= 16 ? 16 / W : 1) ring_norm_grad_kernel(const NormGradArgs a) {
   using R = Row<T, W, true>;
@@ -567,15 +572,18 @@ cudaError_t start_norm_grad(const NormGradArgs& a, const NormShape& s, int grid,
   return launch_pdl(norm_grad_kernel<T, W, NV, VECTOR, LAYER>, dim3(grid), dim3(s.threads), 0, st, a);
 }
 
-// Warps per row of the resident blocks, 0 where one block per row (or warp) runs.
-int ring_warps(int64_t n_rows, int d, int dtype) {
+// Warps per row of the resident blocks for rows of at least min_vecs vectors, 0 where one
+// block per row (or warp) runs.
+int ring_warps(int min_vecs, int d, int dtype) {
   const int V = dtype == MOE_DTYPE_F32 ? 4 : 8;
-  if (n_rows < kRingRows || d % V || d / V <= kRingVecs || d / V > 32 * 32 * kRingNV) return 0;
+  if (d % V || d / V < min_vecs || d / V > 32 * 32 * kRingNV) return 0;
   int W = 4;
   while (d / V > 32 * W * kRingNV) W *= 2;
   return W;
 }
-int ring_grad_grid(int W) { return W >= 16 ? kSms : kSms * 16 / W; }    // 512 threads of an SM
+int ring_grad_grid(int W, int64_t n_rows) {
+  return (int)std::min<int64_t>(n_rows, W >= 16 ? kSms : kSms * 16 / W);        // 512 threads of an SM
+}
 
 // 48 KB of static and dynamic shared memory need no permission
 template <typename K>
@@ -606,7 +614,7 @@ template <typename T, int W, bool LAYER>
 cudaError_t start_ring_grad(const NormGradArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)grad_depth(W) * 3 * kRingNV * 32 * W * 16;
   const cudaError_t e = allow_smem(ring_norm_grad_kernel<T, W, LAYER>, smem);
-  return e != cudaSuccess ? e : launch_pdl(ring_norm_grad_kernel<T, W, LAYER>, dim3(ring_grad_grid(W)), dim3(32 * W),
+  return e != cudaSuccess ? e : launch_pdl(ring_norm_grad_kernel<T, W, LAYER>, dim3(ring_grad_grid(W, a.n_rows)), dim3(32 * W),
                                            smem, st, a);
 }
 template <typename T, bool LAYER>
@@ -623,7 +631,6 @@ cudaError_t start_ring_grad(int W, const NormGradArgs& a, cudaStream_t st) {
       if (s.W == 1) {                                                                   \
         if (s.NV == 1) return F<T, 1, 1, VEC, LAY>(__VA_ARGS__);                        \
         if (s.NV == 2) return F<T, 1, 2, VEC, LAY>(__VA_ARGS__);                        \
-        return F<T, 1, 4, VEC, LAY>(__VA_ARGS__);                                       \
       }                                                                                 \
       MOE_NORM_WIDE(F, T, __VA_ARGS__)                                                  \
       return cudaErrorInvalidValue;                                                     \
@@ -655,6 +662,7 @@ int norm_grad_grid(const NormShape& s, int64_t n_rows) {
 using namespace moe;
 
 #define MOE_NORM_WIDE(F, T, ...)                                     \
+  if (s.W == 1) return F<T, 1, 4, VEC, LAY>(__VA_ARGS__);            \
   if (s.W == 2) return F<T, 2, 4, VEC, LAY>(__VA_ARGS__);            \
   if (s.W == 4) return F<T, 4, 4, VEC, LAY>(__VA_ARGS__);            \
   if (s.W == 8) return F<T, 8, 4, VEC, LAY>(__VA_ARGS__);            \
@@ -679,7 +687,7 @@ extern "C" moe_status moe_layer_norm(const void* x, int32_t dtype, int64_t n_row
   const bool layer = kind == MOE_NORM_LAYER;
   const bool vector = d % (dtype == MOE_DTYPE_F32 ? 4 : 8) == 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int W = ring_warps(n_rows, d, dtype);
+  const int W = n_rows < kRingRows ? 0 : ring_warps(kRingVecs, d, dtype);
   cudaError_t e;
   if (W && dtype == MOE_DTYPE_F32) e = layer ? start_ring<float, true>(W, a, st) : start_ring<float, false>(W, a, st);
   else if (W) e = layer ? start_ring<bf16, true>(W, a, st) : start_ring<bf16, false>(W, a, st);
@@ -694,8 +702,8 @@ extern "C" moe_status moe_layer_norm_backward_workspace_size(int64_t n_rows, int
   size_t parts = 0;
   for (int dtype : {MOE_DTYPE_F32, MOE_DTYPE_BF16}) {
     const NormShape s = norm_shape(d, dtype, kNormGradVecs);
-    const int W = ring_warps(n_rows, d, dtype);
-    const size_t p = W ? (size_t)ring_grad_grid(W) : (size_t)norm_grad_grid(s, n_rows) * s.slots;
+    const int W = ring_warps(kRingGradVecs, d, dtype);
+    const size_t p = W ? (size_t)ring_grad_grid(W, n_rows) : (size_t)norm_grad_grid(s, n_rows) * s.slots;
     parts = p > parts ? p : parts;
   }
   *bytes = kAlign + align_up(parts * 2 * d * 4);
@@ -703,14 +711,17 @@ extern "C" moe_status moe_layer_norm_backward_workspace_size(int64_t n_rows, int
 }
 
 #undef MOE_NORM_WIDE
-#define MOE_NORM_WIDE(F, T, ...)                                              \
-  if (s.W == 2) return F<T, 2, 2, VEC, LAY>(__VA_ARGS__);                     \
-  if (s.W == 4) return F<T, 4, 2, VEC, LAY>(__VA_ARGS__);                     \
-  if (s.W == 8) return F<T, 8, 2, VEC, LAY>(__VA_ARGS__);                     \
-  if (s.W == 16) return F<T, 16, 2, VEC, LAY>(__VA_ARGS__);                   \
-  if (s.W == 32 && s.NV <= 2) return F<T, 32, 2, VEC, LAY>(__VA_ARGS__);      \
-  if constexpr (sizeof(T) == 4) {                                             \
-    if (s.W == 32) return F<T, 32, 4, VEC, LAY>(__VA_ARGS__);                 \
+// rows of whole vectors that take more than a warp run in resident blocks, but for the longest
+#define MOE_NORM_WIDE(F, T, ...)                                                \
+  if constexpr (!VEC) {                                                         \
+    if (s.W == 2) return F<T, 2, 2, VEC, LAY>(__VA_ARGS__);                     \
+    if (s.W == 4) return F<T, 4, 2, VEC, LAY>(__VA_ARGS__);                     \
+    if (s.W == 8) return F<T, 8, 2, VEC, LAY>(__VA_ARGS__);                     \
+    if (s.W == 16) return F<T, 16, 2, VEC, LAY>(__VA_ARGS__);                   \
+    if (s.W == 32 && s.NV <= 2) return F<T, 32, 2, VEC, LAY>(__VA_ARGS__);      \
+  }                                                                             \
+  if constexpr (sizeof(T) == 4) {                                               \
+    if (s.W == 32) return F<T, 32, 4, VEC, LAY>(__VA_ARGS__);                   \
   }
 
 extern "C" moe_status moe_layer_norm_backward(const void* dy, const void* x, int32_t dtype, int64_t n_rows, int32_t d,
@@ -731,8 +742,8 @@ extern "C" moe_status moe_layer_norm_backward(const void* dy, const void* x, int
   if (kind == MOE_NORM_LAYER && !mean) return fail(MOE_ERR_INVALID_ARG, "mean is NULL");
   MOE_CHECK(check_ws(ws, ws_bytes, need));
   const NormShape s = norm_shape(d, dtype, kNormGradVecs);
-  const int W = ring_warps(n_rows, d, dtype);
-  const int grid = W ? ring_grad_grid(W) : norm_grad_grid(s, n_rows);
+  const int W = ring_warps(kRingGradVecs, d, dtype);
+  const int grid = W ? ring_grad_grid(W, n_rows) : norm_grad_grid(s, n_rows);
   const int parts = W ? grid : grid * s.slots;
   float* part = at<float>(ws, kAlign);
   NormGradArgs a{dy, x, dres, gamma, mean, rstd, dx, part, n_rows, d, dgamma || dbeta};

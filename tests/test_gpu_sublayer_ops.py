@@ -71,7 +71,9 @@ def run_norm(x, dtype, kind, gamma, beta, eps=1e-6, tiles=False, out=None):
 # the last line: batches long enough for the blocks that walk the rows, at each of their widths
 NORM_SHAPES = [(1, 1), (3, 7), (5, 8), (4, 64), (33, 100), (300, 256), (17, 1001), (9, 1024), (65, 2048), (12, 2056),
                (6, 4100), (5, 7168), (3, 8200), (3, 16383), (4, 16384), (1, 7168), (601, 16),
-               (593, 520), (700, 1032), (613, 2048), (641, 5000), (597, 7168), (593, 9000), (595, 16384)]
+               (593, 520), (700, 1032), (613, 2048), (641, 5000), (597, 7168), (593, 9000), (595, 16384),
+               # on both sides of the sizes from which rows are walked by resident blocks
+               (443, 1024), (444, 1024), (444, 1016), (450, 512), (2, 512), (150, 504), (1, 256), (149, 256), (2100, 640)]
 
 
 @pytest.mark.parametrize("shape", NORM_SHAPES)
