@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(32 * W, W <= 16 ? 32 / W : 1) ring_norm_kernel
 }
 
 // The backward: gains, the running dgamma and dbeta and the row in registers, one block
-// of 512 threads on an SM: 44 us for 4096 x 7168 bf16 with dres (5.4 TB/s), and 4 for
+// of 512 threads on an SM: 44 us for 4096 x 7168 bf16 with dres (5.3 TB/s), and 4 for
 // the parts' sums.  The row read twice from shared memory with 1024 threads on an SM
 // took 41 instructions a value instead of 28 and 64 us, 1024 threads with one vector
 // each 73 us.  It wins for any number of rows from 64 vectors a row on, where norm_grad_kernel
