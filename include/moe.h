@@ -493,9 +493,9 @@ moe_status moe_quantize_blocks(const void* src, int32_t src_dtype, int32_t n_mat
  *   the same sums, with the tensor core's own order inside 32 products.
  *   out [max_rows, n_cols], out_dtype MOE_DTYPE_BF16 or MOE_DTYPE_F32.  Rows
  *   outside [offsets[0], offsets[n_groups]) are left as they were.
- *   ws: its first 256 bytes zeroed once, and again after an error; offsets out
- *   of order or out of range set its error word (MOE_DEVERR_INDEX) and nothing
- *   is computed.  One workspace serves calls whose work does not overlap on the GPU.
+ *   ws: its first 256 bytes zeroed once, and again after an error
+ *   (moe_clear_device_error); offsets out of order or out of range set its error
+ *   word (MOE_DEVERR_INDEX) and nothing is computed.  One workspace serves calls whose work does not overlap on the GPU.
  */
 moe_status moe_block_matmul_workspace_size(int32_t n_groups, int32_t n_cols, int32_t k,
                                            int32_t max_rows, size_t* bytes);
@@ -579,7 +579,12 @@ moe_status moe_get_device_error(const void* ws, int32_t* code);
  */
 moe_status moe_selftest_bounded_wait(void* ws, int64_t limit_ns, void* stream);
 
-/* Zero the device error word of a workspace (enqueued on stream). */
+/*
+ * Zero the device error word of a workspace and the rest of its control block,
+ * the first 256 bytes, where a call that gave up may have left counters of its
+ * units part-way (enqueued on stream).  ws is a workspace's address; of an
+ * error word that does not begin on 256 bytes the word alone is zeroed.
+ */
 moe_status moe_clear_device_error(void* ws, void* stream);
 
 #ifdef __cplusplus

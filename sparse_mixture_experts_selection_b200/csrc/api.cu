@@ -724,7 +724,10 @@ moe_status moe_selftest_bounded_wait(void* ws, int64_t limit_ns, void* stream) {
 
 moe_status moe_clear_device_error(void* ws, void* stream) {
   if (!ws) return fail(MOE_ERR_INVALID_ARG, "ws is NULL");
-  cudaMemsetAsync(ws, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream));
+  // The control block whole: a call that gave up may have left counters of its units in it.
+  // An address that no workspace has is an error word of its own (moe_ep_plan takes one).
+  const bool block = reinterpret_cast<uintptr_t>(ws) % kAlign == 0;
+  cudaMemsetAsync(ws, 0, block ? kAlign : sizeof(int32_t), static_cast<cudaStream_t>(stream));
   return cuda_status();
 }
 
