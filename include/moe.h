@@ -487,7 +487,7 @@ moe_status moe_quantize_blocks(const void* src, int32_t src_dtype, int32_t n_mat
  *   x [max_rows, k], x_scale [max_rows, ceil(k/128)];  w [n_groups, n_cols, k],
  *   w_scale [n_groups, ceil(n_cols/128), ceil(k/128)];  row_scale [max_rows] float32
  *   or NULL for 1.  k a positive multiple of 16; n_cols >= 1; n_groups <= 1024;
- *   k, n_cols <= 2^20.  out must not overlap an input.
+ *   k, n_cols <= 2^20; max_rows <= 2^31 - 256.  out must not overlap an input.
  *   Groups of at least 768 rows on average run on CTA pairs (256-row tiles), row
  *   tiles of at most 32 rows with the weights as the tensor core's first operand:
  *   the same sums, with the tensor core's own order inside 32 products.

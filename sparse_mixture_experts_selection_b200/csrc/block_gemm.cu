@@ -960,6 +960,8 @@ moe_status check_product(int n_groups, int n_cols, int k, int max_rows) {
   if (n_cols < 1) return fail(MOE_ERR_INVALID_ARG, "n_cols=%d < 1", n_cols);
   if (k < 16 || k % 16) return fail(MOE_ERR_INVALID_ARG, "k=%d must be a positive multiple of 16", k);
   if (max_rows < 0) return fail(MOE_ERR_INVALID_ARG, "max_rows=%d < 0", max_rows);
+  // a group's rows are rounded up to whole tiles in 32 bits
+  if (max_rows > 0x7FFFFFFF - (2 * BM - 1)) return fail(MOE_ERR_UNSUPPORTED, "max_rows=%d above 2^31 - %d", max_rows, 2 * BM);
   if (n_cols > 1 << 20 || k > 1 << 20) return fail(MOE_ERR_UNSUPPORTED, "n_cols=%d k=%d above 2^20", n_cols, k);
   if ((int64_t)n_groups * n_cols > 0x7FFFFFFF) return fail(MOE_ERR_UNSUPPORTED, "n_groups * n_cols above 2^31");
   // units are counted in 32 bits: row tiles x column tiles (of at least 128 columns)

@@ -162,3 +162,15 @@ def test_binding_refuses_tensors_the_kernels_cannot_take():
         moe.moe_dropout_add(x, None, BF, 8, 0.5, torch.zeros(2, dtype=torch.int32), x, stream=0)
     with pytest.raises(moe.MoeError, match="values"):
         moe.moe_block_matmul(3, 16, 64, 8, torch.zeros(3, dtype=torch.int32), x, r, x, r, None, BF, x, r, stream=0)
+
+
+@pytest.mark.parametrize("rows,want", [((1 << 31) - 256, 0), ((1 << 31) - 255, 2), ((1 << 31) - 1, 2)])
+def test_block_products_refuse_rows_that_whole_tiles_carry_past_32_bits(rows, want):
+    """One group of so many rows: rounded up to tiles of 256 rows it must still be counted in 32 bits."""
+    n = ctypes.c_size_t(0)
+    assert status("moe_block_matmul_workspace_size", 1, 16, 16, rows, ctypes.byref(n)) == want
+    assert status("moe_block_ffn_workspace_size", 1, 16, 16, rows, ctypes.byref(n)) == want
+    if want:
+        assert status("moe_block_matmul", 1, 16, 16, rows, None, P, P, P, P, None, BF, P, P, 1 << 40, None) == want
+        assert status("moe_block_ffn", 1, 16, 16, rows, None, *[P] * 8, None, BF, P, P, 1 << 40, None) == want
+        assert b"max_rows" in moe.lib().moe_last_error_detail()
