@@ -467,7 +467,8 @@ moe_status moe_dropout_backward(const void* dy, int32_t dtype, int64_t n, double
  * separate arrays, as such checkpoints store them.  Values must be finite; a NaN
  * becomes the code of NaN.
  *   src [n_rows, cols] or [n_mats, rows, cols] (src_dtype), 16-byte aligned;
- *   cols a positive multiple of 16; rows, cols at most 2^30; codes 16-byte aligned, same shape as src;
+ *   cols a positive multiple of 16; rows, cols at most 2^30, n_rows at most 2^32, and fewer than 2^31
+ *   blocks of 128 x 128 in all (MOE_ERR_UNSUPPORTED above); codes 16-byte aligned, same shape as src;
  *   scales [n_rows, ceil(cols/128)], or [n_mats, ceil(rows/128), ceil(cols/128)].
  */
 moe_status moe_quantize_tiles(const void* src, int32_t src_dtype, int64_t n_rows, int32_t cols,

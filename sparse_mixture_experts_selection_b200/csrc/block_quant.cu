@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const TIn* __restr
 }
 
 constexpr int kMaxSide = 1 << 30;        // rounding up to blocks stays within 32 bits
+constexpr int64_t kMaxRows = (int64_t)1 << 32;     // of tiles: values are counted in 64 bits
 
 moe_status check_source(const void* src, int dtype, int cols, const void* codes, const void* scales, bool empty) {
   if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16) return fail(MOE_ERR_INVALID_ARG, "src_dtype=%d", dtype);
@@ -163,6 +164,7 @@ using namespace moe;
 extern "C" moe_status moe_quantize_tiles(const void* src, int32_t src_dtype, int64_t n_rows, int32_t cols,
                                          uint8_t* codes, float* scales, void* stream) {
   if (n_rows < 0) return fail(MOE_ERR_INVALID_ARG, "n_rows=%lld < 0", (long long)n_rows);
+  if (n_rows > kMaxRows) return fail(MOE_ERR_UNSUPPORTED, "n_rows=%lld > 2^32", (long long)n_rows);
   MOE_CHECK(check_source(src, src_dtype, cols, codes, scales, n_rows == 0));
   if (n_rows == 0) return MOE_OK;
   const cudaError_t e = launch_quantize_tiles(src, src_dtype, n_rows, cols, codes, scales,
@@ -178,8 +180,9 @@ extern "C" moe_status moe_quantize_blocks(const void* src, int32_t src_dtype, in
   MOE_CHECK(check_source(src, src_dtype, cols, codes, scales, empty));
   if (empty) return MOE_OK;
   const int rb = (rows + 127) / 128, cb = (cols + 127) / 128;
-  const int64_t n = (int64_t)n_mats * rb * cb;
-  if (n > 0x7FFFFFFF) return fail(MOE_ERR_UNSUPPORTED, "%lld blocks", (long long)n);
+  const int64_t each = (int64_t)rb * cb;           // below 2^47; times n_mats it may pass 64 bits
+  if (each > 0x7FFFFFFF / n_mats) return fail(MOE_ERR_UNSUPPORTED, "%d matrices of %lld blocks", n_mats, (long long)each);
+  const int64_t n = n_mats * each;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (src_dtype == MOE_DTYPE_BF16)
     quantize_blocks_kernel<uint16_t><<<(unsigned)n, 256, 0, st>>>(static_cast<const uint16_t*>(src), rows, cols, rb,

@@ -174,3 +174,12 @@ def test_block_products_refuse_rows_that_whole_tiles_carry_past_32_bits(rows, wa
         assert status("moe_block_matmul", 1, 16, 16, rows, None, P, P, P, P, None, BF, P, P, 1 << 40, None) == want
         assert status("moe_block_ffn", 1, 16, 16, rows, None, *[P] * 8, None, BF, P, P, 1 << 40, None) == want
         assert b"max_rows" in moe.lib().moe_last_error_detail()
+
+
+def test_quantizers_refuse_sizes_whose_blocks_pass_64_bits():
+    """No memory holds these, but a count of blocks that wraps round looks small."""
+    top = 1 << 30
+    for n_mats, rows, cols in ((1 << 18, top, top), ((1 << 31) - 1, top, top), (1 << 11, 1 << 17, 1 << 17)):
+        assert status("moe_quantize_blocks", P, BF, n_mats, rows, cols, P, P, None) == 2
+    for n_rows, cols in (((1 << 32) + 1, 16), (1 << 58, 16), (1 << 62, top)):
+        assert status("moe_quantize_tiles", P, BF, n_rows, cols, P, P, None) == 2
