@@ -351,7 +351,8 @@ def _pointers(*checks):
     """The addresses of a call's tensors and the device they are on, after a check
     of each (name, tensor, types, number of values).  The kernels take dense
     arrays by pointer, so a strided view, another type, a short tensor or one of
-    another device is refused here.  None and plain addresses pass."""
+    another device is refused here.  None and plain addresses pass (a workspace's
+    size is asked for apart, by _room)."""
     out, device, other = [], None, None
     for name, t, types, n in checks:
         if t is None or t.__class__ is int:
@@ -369,6 +370,13 @@ def _pointers(*checks):
         raise MoeError(1, "the tensors are not on one GPU" + (f" ({other} is on another device)" if other else ""))
     out.append(device)
     return out
+
+
+def _room(ws) -> int:
+    """Bytes of a workspace.  An address alone does not say how many there are."""
+    if ws.__class__ is int:
+        raise MoeError(3, "ws is a plain address, which has no size: pass the tensor")
+    return 0 if ws is None else ws.numel()
 
 
 def _enqueue(fn, device, stream, *args) -> None:
@@ -417,7 +425,7 @@ def moe_layer_norm_backward(dy, x, dtype: int, n_rows: int, d: int, kind: int, g
         ("rstd", rstd, _F32, n_rows), ("dres", dres, act, n), ("dx", dx, act, n), ("dgamma", dgamma, _F32, d),
         ("dbeta", dbeta, _F32, d), ("ws", ws, _BYTES, 0))
     _enqueue(lib().moe_layer_norm_backward, device, stream, p_dy, p_x, dtype, n_rows, d, kind, p_gamma, p_mean,
-             p_rstd, p_dres, p_dx, p_dgamma, p_dbeta, p_ws, ws.numel())
+             p_rstd, p_dres, p_dx, p_dgamma, p_dbeta, p_ws, _room(ws))
 
 
 def moe_dropout_add(x, res, dtype: int, n: int, p: float, rng, out, stream=None):
@@ -471,7 +479,7 @@ def moe_block_matmul(n_groups: int, n_cols: int, k: int, max_rows: int, offsets,
         ("row_scale", row_scale, _F32, max_rows), ("out", out, _ACT.get(out_dtype, _UNKNOWN), max_rows * n_cols),
         ("ws", ws, _BYTES, 0))
     _enqueue(lib().moe_block_matmul, device, stream, n_groups, n_cols, k, max_rows, p_offsets, p_x, p_x_scale, p_w,
-             p_w_scale, p_row_scale, out_dtype, p_out, p_ws, ws.numel())
+             p_w_scale, p_row_scale, out_dtype, p_out, p_ws, _room(ws))
 
 
 def moe_block_ffn_workspace_size(n_experts: int, d_model: int, d_ffn: int, max_rows: int) -> int:
@@ -494,4 +502,4 @@ def moe_block_ffn(n_experts: int, d_model: int, d_ffn: int, max_rows: int, offse
         ("w_down", w_down, _CODES, n), ("s_down", s_down, _F32, nb), ("row_scale", row_scale, _F32, max_rows),
         ("out", out, _ACT.get(out_dtype, _UNKNOWN), max_rows * d_model), ("ws", ws, _BYTES, 0))
     _enqueue(lib().moe_block_ffn, device, stream, n_experts, d_model, d_ffn, max_rows, p_offsets, p_x, p_x_scale,
-             p_w_gate, p_s_gate, p_w_up, p_s_up, p_w_down, p_s_down, p_row_scale, out_dtype, p_out, p_ws, ws.numel())
+             p_w_gate, p_s_gate, p_w_up, p_s_up, p_w_down, p_s_down, p_row_scale, out_dtype, p_out, p_ws, _room(ws))

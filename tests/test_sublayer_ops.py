@@ -183,3 +183,16 @@ def test_quantizers_refuse_sizes_whose_blocks_pass_64_bits():
         assert status("moe_quantize_blocks", P, BF, n_mats, rows, cols, P, P, None) == 2
     for n_rows, cols in (((1 << 32) + 1, 16), (1 << 58, 16), (1 << 62, top)):
         assert status("moe_quantize_tiles", P, BF, n_rows, cols, P, P, None) == 2
+
+
+@pytest.mark.parametrize("ws", [None, P])
+def test_binding_needs_the_size_of_a_workspace(ws):
+    """Plain addresses pass for arrays; a workspace without a size (none at all, or an
+    address alone) is refused as the library refuses one that is too small."""
+    calls = (lambda: moe.moe_layer_norm_backward(P, P, BF, 4, 64, 0, None, P, P, None, P, P, P, ws, stream=0),
+             lambda: moe.moe_block_matmul(1, 16, 64, 4, None, P, P, P, P, None, BF, P, ws, stream=0),
+             lambda: moe.moe_block_ffn(1, 64, 32, 4, None, *[P] * 8, None, BF, P, ws, stream=0))
+    for call in calls:
+        with pytest.raises(moe.MoeError, match="ws is") as e:
+            call()
+        assert e.value.status == 3
