@@ -35,6 +35,12 @@ moe_status cuda_status() {
   return MOE_OK;
 }
 
+moe_status launch_status(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) return MOE_OK;
+  cudaGetLastError();
+  return fail(MOE_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+}
+
 }  // namespace moe
 
 namespace {

@@ -22,6 +22,9 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 moe_status check_ws(const void* ws, size_t ws_bytes, size_t need);
 // MOE_ERR_CUDA with its text when a launch before this call failed.
 moe_status cuda_status();
+// MOE_ERR_CUDA with its text for a launch that returned e.  The runtime's last error is
+// taken too: the next call's cuda_status would report it as its own.
+moe_status launch_status(cudaError_t e, const char* what);
 
 template <typename T> T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);

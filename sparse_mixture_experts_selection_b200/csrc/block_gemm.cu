@@ -999,7 +999,7 @@ extern "C" moe_status moe_block_matmul(int32_t n_groups, int32_t n_cols, int32_t
                                 {x, w, nullptr, x_scale, w_scale, nullptr, row_scale}, false,
                                 out_dtype == MOE_DTYPE_F32, out, nullptr, at<float>(ws, kAlign), at<int>(ws, 0),
                                 static_cast<cudaStream_t>(stream));
-  return e != cudaSuccess ? fail(MOE_ERR_CUDA, "block product launch: %s", cudaGetErrorString(e)) : MOE_OK;
+  return launch_status(e, "block product");
 }
 
 namespace {
@@ -1058,5 +1058,5 @@ extern "C" moe_status moe_block_ffn(int32_t n_experts, int32_t d_model, int32_t 
   if (e == cudaSuccess)
     e = product(n_experts, d_model, d_ffn, max_rows, offsets, {codes, w_down, nullptr, scales, s_down, nullptr, row_scale},
                 false, out_dtype == MOE_DTYPE_F32, out, nullptr, part, ctrl, st);
-  return e != cudaSuccess ? fail(MOE_ERR_CUDA, "block experts launch: %s", cudaGetErrorString(e)) : MOE_OK;
+  return launch_status(e, "block experts");
 }

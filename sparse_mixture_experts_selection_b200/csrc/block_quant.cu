@@ -169,7 +169,7 @@ extern "C" moe_status moe_quantize_tiles(const void* src, int32_t src_dtype, int
   if (n_rows == 0) return MOE_OK;
   const cudaError_t e = launch_quantize_tiles(src, src_dtype, n_rows, cols, codes, scales,
                                               static_cast<cudaStream_t>(stream));
-  return e != cudaSuccess ? fail(MOE_ERR_CUDA, "quantize launch: %s", cudaGetErrorString(e)) : MOE_OK;
+  return launch_status(e, "quantize");
 }
 
 extern "C" moe_status moe_quantize_blocks(const void* src, int32_t src_dtype, int32_t n_mats, int32_t rows,

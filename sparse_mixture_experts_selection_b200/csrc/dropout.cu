@@ -147,7 +147,7 @@ moe_status run_dropout(const void* x, const void* res, int32_t dtype, int64_t n,
                       static_cast<const T*>(x), static_cast<const T*>(res), static_cast<T*>(out), n, last, cut == 0, scale, rng);
   };
   const cudaError_t e = dtype == MOE_DTYPE_F32 ? start(float{}) : start(bf16{});
-  return e != cudaSuccess ? fail(MOE_ERR_CUDA, "dropout launch: %s", cudaGetErrorString(e)) : MOE_OK;
+  return launch_status(e, "dropout");
 }
 
 }  // namespace

@@ -693,7 +693,7 @@ extern "C" moe_status moe_layer_norm(const void* x, int32_t dtype, int64_t n_row
   else if (W) e = layer ? start_ring<bf16, true>(W, a, st) : start_ring<bf16, false>(W, a, st);
   else if (dtype == MOE_DTYPE_F32) e = MOE_NORM_PICK(start_norm, float, a, s, st);
   else e = MOE_NORM_PICK(start_norm, bf16, a, s, st);
-  return e != cudaSuccess ? fail(MOE_ERR_CUDA, "norm launch: %s", cudaGetErrorString(e)) : MOE_OK;
+  return launch_status(e, "norm");
 }
 
 extern "C" moe_status moe_layer_norm_backward_workspace_size(int64_t n_rows, int32_t d, size_t* bytes) {
@@ -756,5 +756,5 @@ extern "C" moe_status moe_layer_norm_backward(const void* dy, const void* x, int
   else e = MOE_NORM_PICK(start_norm_grad, bf16, a, s, grid, st);
   if (e == cudaSuccess && (dgamma || dbeta))
     e = launch_pdl(norm_grad_sum_kernel, dim3((d + 31) / 32, 2), dim3(1024), 0, st, part, parts, d, dgamma, dbeta);
-  return e != cudaSuccess ? fail(MOE_ERR_CUDA, "norm backward launch: %s", cudaGetErrorString(e)) : MOE_OK;
+  return launch_status(e, "norm backward");
 }

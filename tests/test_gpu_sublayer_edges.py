@@ -1,6 +1,8 @@
 """The operators around and inside the expert sublayer at the edges of their
 contract on the GPU: a workspace after an error, values that are not finite,
 arrays that may be the same, whole runs captured and replayed."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -45,3 +47,39 @@ def test_clear_device_error_of_a_lone_word():
     moe.moe_clear_device_error(words[1:2])
     torch.cuda.synchronize()
     assert words.tolist() == [7, 0] + [7] * 126
+
+
+# ---------------------------------------------------------------------------
+# a launch that fails
+# ---------------------------------------------------------------------------
+def test_a_failed_launch_is_reported_by_its_own_call_alone():
+    """Launches into a stream whose capture was cut short fail on the host; each call says
+    so itself, and the next call, which launches nothing, does not report it again."""
+    torch.zeros(1, device="cuda")                   # the primary context is current
+    cu = ctypes.CDLL("libcuda.so.1")
+    x, ws = filled((256,), torch.float32), moe.alloc_workspace(1 << 20)
+    words = torch.zeros(2, dtype=torch.int64, device="cuda")
+    p, stream, graph = x.data_ptr(), ctypes.c_void_p(), ctypes.c_void_p()
+    assert cu.cuStreamCreate(ctypes.byref(stream), 1) == 0
+    try:
+        assert cu.cuStreamBeginCapture_v2(stream, 2) == 0
+        assert cu.cuStreamSynchronize(stream) != 0          # not allowed in a capture, which it ends
+        L, F = moe.lib(), moe.DTYPE_F32
+        calls = {
+            "norm": lambda: L.moe_layer_norm(p, F, 4, 64, 0, None, None, 1e-5, p, None, None, None, None, stream),
+            "norm backward": lambda: L.moe_layer_norm_backward(p, p, F, 4, 64, 1, None, None, p, None, p, None, None,
+                                                               ws.data_ptr(), ws.numel(), stream),
+            "dropout": lambda: L.moe_dropout_add(p, None, F, 256, 0.5, words.data_ptr(), p, stream),
+            "tiles": lambda: L.moe_quantize_tiles(p, F, 4, 64, p, p, stream),
+            "product": lambda: L.moe_block_matmul(1, 16, 16, 4, None, p, p, p, p, None, F, p, ws.data_ptr(), ws.numel(),
+                                                  stream),
+        }
+        for name, call in calls.items():
+            assert call() == 4, name
+            # no rows and no gradients wanted: nothing to launch
+            assert L.moe_layer_norm_backward(None, None, F, 0, 64, 1, *[None] * 8, 0, None) == 0, name
+    finally:
+        cu.cuStreamEndCapture(stream, ctypes.byref(graph))
+        assert cu.cuStreamDestroy_v2(stream) == 0
+    torch.cuda.synchronize()
+    assert (x == -7.0).all()
