@@ -570,13 +570,14 @@ moe_status moe_set_phase_events(void* const* events, int32_t n_events);
 moe_status moe_get_device_error(const void* ws, int32_t* code);
 
 /*
- * Failure-detection self-test.  Enqueues one kernel whose only thread waits,
- * through the same bounded shared-memory-barrier wait every GEMM pipeline
- * stage uses, on a barrier that nothing ever arrives on.  After limit_ns
- * (1 ms .. 2 s) the wait gives up, writes MOE_DEVERR_WAIT_TIMEOUT into the
- * error word of ws (the first 256 bytes of a workspace) and the kernel
- * returns: no trap, no hang, the context stays usable.  Read the word with
- * moe_get_device_error after synchronising the stream.
+ * Failure-detection self-test.  Enqueues one kernel whose only thread waits on
+ * a shared-memory barrier that nothing ever arrives on, through the two bounded
+ * waits of the GEMM pipelines in turn: the one of the layer's GEMMs and the one of
+ * the block products (CTA pairs run the same loops and tell the other CTA to stop
+ * as well).  After limit_ns (1 ms .. 2 s) each gives up; when both did, the kernel
+ * writes MOE_DEVERR_WAIT_TIMEOUT into the error word of ws (the first 256 bytes of a
+ * workspace) and returns: no trap, no hang, the context stays usable.  Read the
+ * word with moe_get_device_error after synchronising the stream.
  */
 moe_status moe_selftest_bounded_wait(void* ws, int64_t limit_ns, void* stream);
 

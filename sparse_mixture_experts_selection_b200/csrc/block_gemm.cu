@@ -224,7 +224,7 @@ __device__ __forceinline__ void scan_groups(const BlockArgs& a, Control* c) {
 // cluster scope in every block took three times the time).
 template <bool PAIR>
 __device__ __forceinline__ bool block_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err,
-                                           uint32_t peer_abort) {
+                                           uint32_t peer_abort, uint64_t limit_ns = kWaitLimitNs) {
   uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -232,7 +232,7 @@ __device__ __forceinline__ bool block_wait(uint64_t* bar, uint32_t parity, volat
       if (*abort) return false;
       const uint64_t now = global_timer_ns();
       if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitLimitNs) {
+      if (now - t0 > limit_ns) {
         set_device_error(err, MOE_DEVERR_WAIT_TIMEOUT);
         *abort = 1;
         if constexpr (PAIR) st_remote_u32(peer_abort, 1u);
@@ -835,6 +835,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
   }
 }
 
+// Failure-detection self-test: one thread waits on a barrier that nothing arrives on, first
+// through the wait of the layer's GEMMs, then through that of the block products; the error
+// word is set when both gave up, recorded it and told the other roles.
+__global__ void bounded_wait_selftest_kernel(uint64_t limit_ns, int* err) {
+  __shared__ uint64_t bar;
+  __shared__ int abort_flag, code;
+  if (threadIdx.x != 0) return;
+  mbar_init(&bar, 1);
+  fence_barrier_init();
+  bool gave_up = true;
+  for (int which = 0; which < 2; ++which) {
+    abort_flag = code = 0;
+    const bool done = which == 0 ? mbar_wait(&bar, 0, &abort_flag, &code, limit_ns)
+                                 : block_wait<false>(&bar, 0, &abort_flag, &code, 0, limit_ns);
+    gave_up = gave_up && !done && abort_flag == 1 && code == MOE_DEVERR_WAIT_TIMEOUT;
+  }
+  if (gave_up) set_device_error(err, MOE_DEVERR_WAIT_TIMEOUT);
+}
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -971,6 +990,11 @@ moe_status check_product(int n_groups, int n_cols, int k, int max_rows) {
 }
 
 }  // namespace
+
+void launch_bounded_wait_selftest(uint64_t limit_ns, int* err, cudaStream_t st) {
+  bounded_wait_selftest_kernel<<<1, 32, 0, st>>>(limit_ns, err);
+}
+
 }  // namespace moe
 
 using namespace moe;

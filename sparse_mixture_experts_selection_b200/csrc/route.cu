@@ -861,18 +861,6 @@ stats_final_kernel(const float* __restrict__ pchunk, const int* __restrict__ seq
   }
 }
 
-// Failure-detection self-test: one thread waits, through the same bounded
-// mbarrier wait the GEMM pipelines use, on a barrier nothing arrives on.
-__global__ void bounded_wait_selftest_kernel(uint64_t limit_ns, int* err) {
-  __shared__ uint64_t bar;
-  __shared__ int abort_flag;
-  if (threadIdx.x != 0) return;
-  abort_flag = 0;
-  mbar_init(&bar, 1);
-  fence_barrier_init();
-  mbar_wait(&bar, 0, &abort_flag, err, limit_ns);     // never completes: times out
-}
-
 // ---------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------
@@ -892,9 +880,6 @@ void launch_router_stats(const float* s, const float* z, const int32_t* idx, con
                                          seq_len, n_ch, use_seq, alpha_aux, c_z, alpha_seq, stats);
 }
 
-void launch_bounded_wait_selftest(uint64_t limit_ns, int* err, cudaStream_t st) {
-  bounded_wait_selftest_kernel<<<1, 32, 0, st>>>(limit_ns, err);
-}
 void launch_router_logits(const void* h, int dtype, const float* e, float* z, int T, int d, int E,
                           cudaStream_t st) {
   dim3 grid((T + 63) / 64, (E + 63) / 64);

@@ -83,3 +83,17 @@ def test_a_failed_launch_is_reported_by_its_own_call_alone():
         assert cu.cuStreamDestroy_v2(stream) == 0
     torch.cuda.synchronize()
     assert (x == -7.0).all()
+
+
+def test_both_bounded_waits_run_out():
+    """The self-test goes through the wait of the layer's GEMMs and that of the block
+    products: it takes the limit twice, and the error word says that both gave up."""
+    ws = moe.alloc_workspace(256)
+    limit_ms = 20
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    moe.moe_selftest_bounded_wait(ws, limit_ms * 1_000_000)
+    end.record()
+    torch.cuda.synchronize()
+    assert moe.moe_get_device_error(ws) == moe.DEVERR_WAIT_TIMEOUT
+    assert start.elapsed_time(end) >= 2 * limit_ms
