@@ -196,3 +196,26 @@ def test_binding_needs_the_size_of_a_workspace(ws):
         with pytest.raises(moe.MoeError, match="ws is") as e:
             call()
         assert e.value.status == 3
+
+
+# the generator's other two published known answers: counter, key, words
+PHILOX_ANSWERS = [
+    ("ffffffff ffffffff ffffffff ffffffff", "ffffffff ffffffff", "408f276d 41c83b0e a20bc7c6 6d5451fd"),
+    ("243f6a88 85a308d3 13198a2e 03707344", "a4093822 299f31d0", "d16cfe09 94fdcceb 5001e420 24126ea1"),
+]
+
+
+@pytest.mark.parametrize("counter,key,words", PHILOX_ANSWERS)
+def test_philox_published_words_and_their_order(counter, key, words):
+    """The published answers, and through them the order in which the seed, the number of the
+    draw and a value's place fill the key and the counter: low words first."""
+    c, k, w = ([int(v, 16) for v in t.split()] for t in (counter, key, words))
+    assert ref.philox(np.array([c], np.uint64), k)[0].tolist() == w
+    seed, draw, block = k[0] | k[1] << 32, c[2] | c[3] << 32, c[0] | c[1] << 32
+    for p in (0.25, 0.5, 0.9):
+        want = [v / 2.0 ** 32 >= p for v in w]
+        assert ref.keep_mask(seed, draw, 4, p, first=4 * block).tolist() == want
+    # words above and below each of them, one after the other
+    for i in range(4):
+        assert ref.keep_mask(seed, draw, 4, w[i] / 2.0 ** 32, first=4 * block)[i]
+        assert not ref.keep_mask(seed, draw, 4, (w[i] + 1) / 2.0 ** 32, first=4 * block)[i]
