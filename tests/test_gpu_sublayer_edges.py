@@ -7,11 +7,12 @@ import numpy as np
 import pytest
 import torch
 
+import moe_inputs as mi
 import sparse_mixture_experts_selection_b200 as moe
 import sublayer_reference as ref
-from sublayer_reference import blocks
-from test_gpu_sublayer_ops import (CODE, TORCH, check_matmul, codes_of, dev, ffn_weights, filled, host, norm_inputs, operands,
-                                   rounded, run_norm)
+from sublayer_reference import U32, blocks, half_step
+from test_gpu_sublayer_ops import (CODE, TORCH, check_matmul, close, codes_of, dev, ffn_weights, filled, host, norm_inputs,
+                                   operands, rounded, run_norm, small_layer)
 
 pytestmark = pytest.mark.gpu
 
@@ -261,3 +262,204 @@ def test_block_ffn_of_nan_codes(rows, d, f):
     out = run(xc, B)
     assert torch.isnan(out[mine, d - 1]).all() and torch.equal(out[mine, :d - 1], clean[mine, :d - 1])
     assert torch.equal(out[:mine.start], clean[:mine.start])
+
+
+# ---------------------------------------------------------------------------
+# captured and replayed
+# ---------------------------------------------------------------------------
+def captured(step):
+    """A graph of the calls of step, made once before."""
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    return graph
+
+
+def test_serving_sublayer_captured_and_replayed():
+    """norm with its e4m3 copy, routing, the gather of codes and scales, routed and shared
+    block-scaled experts and the combine as one graph: replays with new rows give what
+    the calls give."""
+    w, W, _ = small_layer()
+    T, d, f, fs, E, K = w.T, w.d_model, w.d_ffn, w.d_ffn_shared, w.E_r, w.K
+    rng = np.random.default_rng(72)
+    BF = torch.bfloat16
+    cfg = moe.config_for(w)
+    ws = moe.alloc_workspace(moe.moe_workspace_size(cfg))
+    wf = moe.alloc_workspace(max(moe.moe_block_ffn_workspace_size(E, d, f, T * K),
+                                 moe.moe_block_ffn_workspace_size(1, d, fs, T)))
+    D = {}
+    for k, v in W.items():
+        n, r, c = v.shape
+        D[k] = (filled((n, r, c), torch.uint8, 0), filled((n, blocks(r), blocks(c)), torch.float32))
+        moe.moe_quantize_blocks(dev(v, BF), moe.DTYPE_BF16, n, r, c, *D[k])
+    x, gamma = filled((T, d), BF), dev(rng.uniform(0.5, 1.5, size=d))
+    e, b = dev(mi.gen_centroids(w)), dev(mi.gen_bias(w))
+    h, codes, scales = filled((T, d), BF), filled((T, d), torch.uint8, 0), filled((T, blocks(d)), torch.float32)
+    i32 = lambda *sh: filled(sh, torch.int32, -5)  # noqa: E731
+    idx, gates, counts = i32(T, K), filled((T, K), torch.float32), i32(E)
+    off, tok, row_of, kept, rg = i32(E + 1), i32(T * K), i32(T, K), i32(E), filled((T * K,), torch.float32)
+    cp, sp = filled((T * K, d), torch.uint8, 0), filled((T * K, blocks(d)), torch.float32)
+    slot, shared, y = filled((T * K, d), BF), filled((1, T, d), BF), filled((T, d), BF)
+
+    def step():
+        moe.moe_layer_norm(x, moe.DTYPE_BF16, T, d, moe.NORM_RMS, gamma, None, 1e-6, h, None, None, codes, scales)
+        moe.moe_route(cfg, h, e, b, None, None, idx, gates, counts, ws)
+        moe.moe_permute(cfg, idx, gates, None, off, tok, row_of, kept, rg, None, ws)
+        moe.moe_gather_rows(codes, T, d, tok, T * K, cp)
+        moe.moe_gather_rows(scales, T, 4 * blocks(d), tok, T * K, sp)
+        moe.moe_block_ffn(E, d, f, T * K, off, cp, sp, *D["gate"], *D["up"], *D["down"], rg, moe.DTYPE_BF16, slot, wf)
+        moe.moe_block_ffn(1, d, fs, T, None, codes, scales, *D["sgate"], *D["sup"], *D["sdown"], None, moe.DTYPE_BF16,
+                          shared, wf)
+        moe.moe_combine(cfg, x, slot, shared, row_of, y)
+
+    fresh = lambda: x.copy_(dev(rng.normal(size=(T, d)) * 3.0, BF))  # noqa: E731
+    fresh()
+    graph = captured(step)
+    seen = []
+    for _ in range(3):
+        fresh()
+        y.fill_(-7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        seen.append((y.clone(), idx.clone()))
+        for t in (y, slot, shared):
+            t.fill_(-7.0)
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(y, seen[-1][0]) and torch.equal(idx, seen[-1][1])
+    assert not torch.equal(seen[0][0], seen[1][0]) and torch.isfinite(seen[0][0]).all()
+    assert moe.moe_get_device_error(wf) == 0 and moe.moe_get_device_error(ws) == 0
+
+
+def test_cta_pairs_captured_and_replayed():
+    """A product and experts on CTA pairs (launched as clusters) as one graph; the replay's
+    offsets are others than the capture's."""
+    rng = np.random.default_rng(73)
+    n, k, R = 4400, 384, 2048
+    v, s = operands(rng, R, k)
+    w, wsc = operands(rng, n, k, 1)
+    args = [codes_of(v), dev(s), codes_of(w), dev(wsc)]
+    d, f, Rf = 2320, 1168, 4101
+    W = [(codes_of(a), dev(b)) for a, b in ffn_weights(rng, 2, d, f)]
+    xq, xs = ref.quantize_tiles(rounded(rng.normal(size=(Rf, d)), "bf16"))
+    xq, xs = codes_of(xq), dev(xs)
+    off1, off2 = dev([0, R], torch.int32), dev([0, 3001, 4101], torch.int32)
+    out, y = filled((R, n), torch.bfloat16), filled((Rf, d), torch.bfloat16)
+    ws = moe.alloc_workspace(max(moe.moe_block_matmul_workspace_size(1, n, k, R),
+                                 moe.moe_block_ffn_workspace_size(2, d, f, Rf)))
+
+    def step():
+        moe.moe_block_matmul(1, n, k, R, off1, *args, None, moe.DTYPE_BF16, out, ws)
+        moe.moe_block_ffn(2, d, f, Rf, off2, xq, xs, *W[0], *W[1], *W[2], None, moe.DTYPE_BF16, y, ws)
+
+    graph = captured(step)
+    for a, b in (([5, 2000], [0, 1, 4101]), ([0, 2048], [100, 100, 100]), ([0, 2048], [0, 3001, 4101])):
+        off1.copy_(dev(a, torch.int32)), off2.copy_(dev(b, torch.int32))
+        got = []
+        for go in (graph.replay, step):
+            out.fill_(-7.0), y.fill_(-7.0)
+            go()
+            torch.cuda.synchronize()
+            got.append((out.clone(), y.clone()))
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+        assert (out[:a[0]] == -7.0).all() and (out[a[1]:] == -7.0).all() and torch.isfinite(out).all()
+        assert (y[:b[0]] == -7.0).all() and (y[b[2]:] == -7.0).all()
+    assert moe.moe_get_device_error(ws) == 0
+
+
+def test_two_graphs_share_a_workspace():
+    """Cut products captured in two graphs with one workspace, replayed in turn, and a
+    norm's backward between them: the counters are back at zero behind each."""
+    rng = np.random.default_rng(74)
+    ops = []
+    need = moe.moe_layer_norm_backward_workspace_size(300, 512)
+    for rows, n, k in ((3, 1500, 7168), (90, 700, 4096)):
+        v, s = operands(rng, rows, k)
+        w, wsc = operands(rng, n, k, 1)
+        need = max(need, moe.moe_block_matmul_workspace_size(1, n, k, rows))
+        ops.append((rows, n, k, v, s, w, wsc, [codes_of(v), dev(s), codes_of(w), dev(wsc)], filled((rows, n), torch.float32)))
+    ws = moe.alloc_workspace(need)
+    graphs = []
+    for rows, n, k, _, _, _, _, t, out in ops:
+        graphs.append(captured(lambda: moe.moe_block_matmul(1, n, k, rows, None, *t, None, moe.DTYPE_F32, out, ws)))
+    x, r = dev(rng.normal(size=(300, 512))), dev(np.ones(300))
+    dx, dg = torch.empty_like(x), filled((512,), torch.float32)
+    for _ in range(2):
+        for graph, op in zip(graphs + graphs[::-1], ops + ops[::-1]):
+            op[-1].fill_(-7.0)
+            graph.replay()
+            moe.moe_layer_norm_backward(x, x, moe.DTYPE_F32, 300, 512, moe.NORM_RMS, None, None, r, None, dx, dg, None, ws)
+            torch.cuda.synchronize()
+            assert not ws[:256].any()
+            check_matmul(op[-1], op[3], op[4], op[5], op[6], [0, op[0]], "f32")
+
+
+# ---------------------------------------------------------------------------
+# places that pass 32 bits
+# ---------------------------------------------------------------------------
+def test_dropout_of_more_than_2_32_values():
+    """The counter and the addresses behind 2^32 values, in place."""
+    n, p, seed, draw = (1 << 32) + 4099, 0.25, 77, 5
+    words = torch.tensor([seed, draw], dtype=torch.int64, device="cuda")
+    x = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    moe.moe_dropout_backward(x, moe.DTYPE_BF16, n, p, words, x)
+    for first in (0, (1 << 31) - 2048, (1 << 32) - 2048, n // 4 * 4 - 4096):
+        got = host(x[first:first + 4096]) != 0
+        assert np.array_equal(got, ref.keep_mask(seed, draw, got.size, p, first=first))
+    assert bool(x[-1] != 0) == bool(ref.keep_mask(seed, draw, 3, p, first=n - 3)[-1])
+
+
+def test_norm_and_tiles_of_more_than_2_32_values():
+    """Rows behind the 2^32nd value, in the norm with its copy, its backward and the tile
+    quantizer, are the same as those rows by themselves."""
+    d = 7168
+    n = (1 << 32) // d + 60
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    x = torch.empty((n, d), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    gamma = torch.rand(d, generator=g, device="cuda") + 0.5
+    out, rstd = torch.empty_like(x), torch.empty(n, device="cuda")
+    codes, scales = torch.empty((n, d), dtype=torch.uint8, device="cuda"), torch.empty((n, blocks(d)), device="cuda")
+    T = moe.DTYPE_BF16
+    moe.moe_layer_norm(x, T, n, d, moe.NORM_RMS, gamma, None, 1e-6, out, None, rstd, codes, scales)
+    few = slice(n - 600, n)            # enough for the same blocks that walk the rows
+
+    def same(rows, values, what):
+        assert torch.equal(rows[few], values), what
+
+    o2, r2, c2, s2 = out[few].clone(), rstd[few].clone(), codes[few].clone(), scales[few].clone()
+    for t in (o2, r2, c2, s2):
+        t.zero_()
+    moe.moe_layer_norm(x[few].clone(), T, 600, d, moe.NORM_RMS, gamma, None, 1e-6, o2, None, r2, c2, s2)
+    same(out, o2, "out"), same(rstd, r2, "rstd"), same(codes, c2, "codes"), same(scales, s2, "scales")
+    codes.zero_(), scales.zero_()
+    moe.moe_quantize_tiles(out, T, n, d, codes, scales)
+    same(codes, c2, "tiles"), same(scales, s2, "tile scales")
+    ws = moe.alloc_workspace(moe.moe_layer_norm_backward_workspace_size(n, d))
+    moe.moe_layer_norm_backward(out, x, T, n, d, moe.NORM_RMS, gamma, None, rstd, None, out, None, None, ws)
+    moe.moe_layer_norm_backward(o2, x[few].clone(), T, 600, d, moe.NORM_RMS, gamma, None, r2, None, o2, None, None, ws)
+    same(out, o2, "dx")
+
+
+@pytest.mark.parametrize("groups,n,R", [(1, 2048, (1 << 21) + 300), (1024, 5600, 780_000)])
+def test_block_matmul_of_more_than_2_32_values(groups, n, R):
+    """Rows of the output behind the 2^32nd value: one group on CTA pairs, and as many
+    rows in 1024 groups, 762 each, on single CTAs."""
+    k = 16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    codes = lambda *sh: torch.randint(0, 0x7F, sh, generator=g, device="cuda", dtype=torch.uint8)  # noqa: E731
+    scales = lambda *sh: torch.rand(sh, generator=g, device="cuda") + 0.5  # noqa: E731
+    x, xs, w, wsc = codes(R, k), scales(R, 1), codes(groups, n, k), scales(groups, blocks(n), 1)
+    off = torch.linspace(0, R, groups + 1, device="cuda", dtype=torch.float64).to(torch.int32)
+    off[0], off[-1] = 0, R
+    out = torch.zeros((R, n), dtype=torch.bfloat16, device="cuda")
+    ws = moe.alloc_workspace(moe.moe_block_matmul_workspace_size(groups, n, k, R))
+    moe.moe_block_matmul(groups, n, k, R, off, x, xs, w, wsc, None, moe.DTYPE_BF16, out, ws)
+    torch.cuda.synchronize()
+    assert moe.moe_get_device_error(ws) == 0
+    few = slice(R - 300, R)
+    y, size = ref.product(ref.E4M3[x[few].cpu().numpy()], host(xs[few]), ref.E4M3[w[-1].cpu().numpy()], host(wsc[-1]))
+    close(host(out[few]), y, (ref.product_slack(k) + 2 * U32) * size + (half_step("bf16") + U32) * np.abs(y))
