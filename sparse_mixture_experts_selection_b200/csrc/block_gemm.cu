@@ -105,7 +105,7 @@ struct Control {
   alignas(16) float xs[EPI_WARPS][CHUNK][kSwapRows / 2];   // transposed: scales of a warp's 16 rows
   uint64_t full[MAX_STAGES], done[MAX_STAGES], slot_empty[SLOTS], drain;
   uint32_t tmem;
-  int abort, last, total;
+  int abort, last;
   int warp_sum[NUM_THREADS / 32];
   float top[4][BM];                                 // SwiGLU: maxima of the parts of a row's tile
   int prefix[kMaxGroups + 1];                       // units of the groups before
@@ -118,7 +118,7 @@ int blocks_of(int n) { return (n + kBlock - 1) / kBlock; }
 
 struct BlockArgs {
   CUtensorMap x, x32, w0, w1;       // rows in boxes of 128 and 32; weights in boxes of 128, or 64 for a pair (gate, up)
-  int G, N, K, max_rows;
+  int G, N, max_rows;
   int KB, NB, NT;                   // blocks of the reduction and of the columns; column tiles
   int ranges, per;                  // ranges of the reduction, blocks per range
   const int* offsets;
@@ -512,7 +512,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) block_product_kernel(const __g
   if (warp == 1 && lane == 0) { prefetch_tmap(&a.x); prefetch_tmap(&a.x32); prefetch_tmap(&a.w0); prefetch_tmap(&a.w1); }
   __syncthreads();
   if constexpr (PAIR) {
-    __syncthreads();
     cluster_sync_all();        // both CTAs' barriers are initialised before either signals the other
     if (warp == 0) tmem_alloc_pair(&c->tmem, TMEM_COLS);
   } else if (warp == 0) {
@@ -908,7 +907,8 @@ Cut cut_of(int n_groups, int n_cols, int k, int max_rows, bool swiglu) {
   const int most = max_rows <= kSwapRows ? MAX_RANGES : MAX_RANGES_LONG;
   const int64_t want = c.tiles > 0 ? kSms / c.tiles : 1;
   c.per = kb;
-  if (want >= 2 && c.tiles <= MAX_CUT_TILES && kb >= 4)
+  static_assert(kSms / 2 <= MAX_CUT_TILES, "a counter for every cut tile");
+  if (want >= 2 && kb >= 4)
     c.per = std::max({2, (int)((kb + want - 1) / want), (kb + most - 1) / most});
   c.ranges = (kb + c.per - 1) / c.per;
   return c;
@@ -931,7 +931,7 @@ cudaError_t product(int G, int N, int K, int max_rows, const int* offsets, const
   if (!tensor_map(&a.x, o.x, max_rows, K, BM) || !tensor_map(&a.x32, o.x, max_rows, K, SUB_ROWS) ||
       !tensor_map(&a.w0, o.w0, (uint64_t)G * N, K, box) || !tensor_map(&a.w1, w1, (uint64_t)G * N, K, box))
     return cudaErrorInvalidValue;
-  a.G = G; a.N = N; a.K = K; a.max_rows = max_rows;
+  a.G = G; a.N = N; a.max_rows = max_rows;
   a.KB = blocks_of(K); a.NB = blocks_of(N); a.NT = cut.nt;
   a.ranges = cut.ranges; a.per = cut.per;
   a.offsets = offsets;

@@ -142,8 +142,6 @@ moe_status check_source(const void* src, int dtype, int cols, const void* codes,
   return MOE_OK;
 }
 
-}  // namespace
-
 cudaError_t launch_quantize_tiles(const void* src, int src_dtype, int64_t n_rows, int cols, uint8_t* codes,
                                   float* scales, cudaStream_t st) {
   const int tiles = (cols + 127) / 128;
@@ -157,6 +155,7 @@ cudaError_t launch_quantize_tiles(const void* src, int src_dtype, int64_t n_rows
                     tiles, cols, codes, scales);
 }
 
+}  // namespace
 }  // namespace moe
 
 using namespace moe;

@@ -82,10 +82,6 @@ void launch_quantize_rows(const void* src, int src_dtype, const int32_t* src_row
                           const int* n_rows_ptr, int64_t n_rows, int cols, uint8_t* codes,
                           float* scales, int* err, cudaStream_t st);
 
-// the same codes with one scale for each 1 x 128 tile: scales [n_rows, ceil(cols/128)]
-cudaError_t launch_quantize_tiles(const void* src, int src_dtype, int64_t n_rows, int cols, uint8_t* codes,
-                                  float* scales, cudaStream_t st);
-
 int simt_bm();
 int simt_bn();
 void launch_ffn_simt(const FfnArgs& a, int which, cudaStream_t st);
