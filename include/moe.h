@@ -67,6 +67,8 @@
 extern "C" {
 #endif
 
+/* Raised when an entry point changes for a caller built against the header before;
+ * one that is only added, found by its name, need not raise it. */
 #define MOE_ABI_VERSION 4
 
 typedef enum {

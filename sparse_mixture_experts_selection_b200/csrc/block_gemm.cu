@@ -19,24 +19,28 @@
 // are N = 256: a block takes two of the four slots of 128 columns of tensor memory.  A shorter
 // tile runs transposed, each block of weights an M = 128 operand and the rows,
 // rounded up to 16, N: one slot, so four blocks are on their way, and no padding
-// rows in the epilogue (2048 x 7168 weights, one row: 22 against 61 us; 150 experts of 4
-// rows: 364 against 374; 64 experts of 32 rows: 185 both).  Tiles of up to 64 rows are no faster
-// that way (64 experts of 64 rows, 1400 x 2032: 65 against 58 us): the weights still pass
-// shared memory whole.
+// rows in the epilogue (2048 x 7168 weights, one row: 11.1 us, as a plain tile 18.5; 150 experts
+// of 4 rows: 353 and 368; 64 experts of 32 rows: 170 and 172).  Tiles of up to 64 rows were no faster
+// that way (64 experts of 64 rows, 1400 x 2032: 65 against 58 us a call by itself): the weights
+// still pass shared memory whole.
+//
+// Times here are of calls over inputs in turn, on the device, unless they say "a call by
+// itself": that is one with the L2 flushed before it, which takes 5 us longer.
 //
 // What bounds a block of 128 rows is the way of its sums through the accumulator warps, not the
-// tensor cores (512 cycles) nor the loads (20 KB of the 48 left out: 536 instead of 558 us).  Of
-// about 1220 cycles on a single CTA the warps read tensor memory and add for 445, release it and
-// add the last sums for 180, prepare scales and the next wait for 120, wait for the tensor cores
-// for 175, and a unit's epilogue comes to 185 for each of its 32 blocks.
+// tensor cores (512 cycles) nor the loads (20 KB of the 48 left out: 536 instead of 558 us a call
+// by itself).  Of about 1220 cycles on a single CTA the warps read tensor memory and add for 445,
+// release it and add the last sums for 180, prepare scales and the next wait for 120, wait for the
+// tensor cores for 175, and a unit's epilogue comes to 185 for each of its 32 blocks; the other
+// 115 were not taken apart.
 //
 // Groups of many rows run on clusters of two CTAs (cta_group::2) in units of 256 rows:
 // each CTA holds its half of the rows and half of the weight rows, so a block takes 32 KB of
 // its shared memory, and of the way there from L2, instead of 48.
-// 14336 x 4096 weights, single CTAs against pairs: 8 groups of 1024 rows 543 and 485 us, of
-// 768 rows 416 and 370, of 512 rows 287 and 257, one of 768 rows 75 and 66.  A tile of 256 that
-// is not full costs more than one of 128: one group of 640 rows 54 and 66 us, 256 groups of 128
-// rows (2048 x 7168) 684 and 940.  The launch knows the groups' sum alone, and of ragged groups
+// 14336 x 4096 weights, single CTAs against pairs: 8 groups of 1024 rows 550 and 499 us, of
+// 768 rows 477 and 411, of 512 rows 316 and 291, one of 768 rows 74 and 66.  A tile of 256 that
+// is not full costs more than one of 128: one group of 640 rows 51 and 63 us, 256 groups of 128
+// rows (2048 x 7168) 702 and 987.  The launch knows the groups' sum alone, and of ragged groups
 // the last tiles are half empty: 128 rows a group with pairs, 64 without.  From 768 rows a
 // group on pairs' gain of a tenth is more than that.
 //
@@ -44,9 +48,13 @@
 // each unit of a range leaves its accumulators in the workspace, and the last
 // unit of a tile to finish adds the ranges in ascending order (so the sum
 // does not depend on which one was last) and runs the epilogue.  That one CTA has all ranges
-// to read, 128 KB each when all rows are there, so few are better than one for every SM: 2048 x
-// 7168 weights, 64 rows: 48 us with 18 ranges, 30 with 8, 26 with 6, 32 with 4; one row: 19 us with 18,
-// 17 with 8, 19 with 6, 22 with 4.
+// to read, 128 KB each when all rows are there, so few are better than one for every SM.  With at
+// most 4, 6, 8 and 12 ranges (us):
+//   one row   2048 x 7168: 14.3 12.4 11.0 10.8;  4096 x 14336: 22.5 18.6 17.6 17.5;  256 x 16384: 22.5 17.9 14.6 12.6
+//   32 rows   2048 x 7168: 17.3 15.8 15.1 16.2;  4096 x 14336: 26.6 22.7 22.0 22.7;  256 x 16384: 26.6 22.2 18.7 18.0
+//   64 rows   2048 x 7168: 20.5 19.8 23.3 24.2;  4096 x 14336: 30.0 27.3 30.4 30.5;  256 x 16384: 29.2 25.7 25.6 26.2
+//   300 rows  2048 x 7168: 25.4 26.5 28.4 28.6;  4096 x 14336: 39.8 39.6 41.8 42.7;  256 x 16384: 33.0 32.3 32.0 32.0
+// and 7168 x 2048, whose tiles leave room for five at most, 10.1 to 20 with each.
 //
 // Warp roles (384 threads): warp 0 = TMA producer (+ tensor memory), warp 1 = MMA
 // issuer, warps 4 .. 11 = accumulators and epilogue: warp w reads
@@ -55,7 +63,7 @@
 // four warps (2 and 3 only fill their warpgroup) give up registers for that (setmaxnreg).
 // Each thread fetches the scales of its own row, four blocks at a time and four blocks
 // ahead, into registers.  Two warps that staged them in shared memory for all, with a barrier
-// each way, cost 8 x 1024 rows 587 us instead of 522.
+// each way, cost 8 x 1024 rows 587 us instead of 522 (a call by itself).
 #include <algorithm>
 #include <type_traits>
 #include <cuda.h>
@@ -87,7 +95,7 @@ static_assert(kSwapRows == 32, "a transposed tile's rows: 16 to each half of the
 constexpr int EPI_WARPS = 8;
 constexpr int NUM_THREADS = 128 + 32 * EPI_WARPS;
 constexpr int EPI_THREAD0 = 128;
-// 3 x 128 threads are launched with 168 registers each: 128 x 72 + 256 x 216 are as many
+// 3 x 128 threads are launched with 168 registers each: 128 x 40 + 256 x 232 are as many
 constexpr int FEW_REGS = 40, MANY_REGS = 232;
 static_assert(128 * FEW_REGS + 32 * EPI_WARPS * MANY_REGS <= NUM_THREADS * 168, "registers of the launch");
 constexpr int TMEM_COLS = 512;

@@ -370,10 +370,13 @@ __global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W) norm_grad_kernel(const 
 // gains stay in registers.  One block per row instead reads the gains again with each
 // row and has no load in flight while it sums: 47 against 27 us for 4096 x 7168 bf16
 // (4.3 TB/s; a plain copy of that size takes 21 us), and depth 4 or 6 takes 31 or 33.
-// From three rows an SM on (bf16, 7168 columns, ring and block per row: 296 rows 10.2 us both, 444 rows
-// 10.2 and 12.3, 1184 rows 14.3 and 20.5) and rows of 128 16-byte vectors (8192 rows of 1024 columns
-// 16.4 and 18.5, of 512 columns 16.4 and 12.3: half of the threads have none).
-// What bounds it now is issuing: 20 instructions a value, 69 % of the slots.
+// From three rows an SM on (bf16, 7168 columns, ring and block per row: 296 rows 4.2 and 4.7 us, 444 rows
+// 5.8 and 8.0, 1184 rows 9.1 and 15.3) and rows of 128 16-byte vectors (8192 rows of 1024 columns
+// 11.8 and 14.2, of 512 columns 10.8 and 6.4: half of the threads have none).
+// What it uses most of now are issue slots, 69 % (20 instructions a value; the rms kind, with
+// fewer of them and one sum a row instead of two, takes 20 us); neither they nor memory are at
+// their limit.  fp32, with half the instructions a byte: 42 us, 5.6 TB/s.
+// Times are of calls over inputs in turn, on the device; one by itself with a cold L2 takes 4 to 6 us longer.
 __device__ __forceinline__ void copy16(void* smem, const void* global, bool in) {
   const int bytes = in ? 16 : 0;                       // 0: zeros are written
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem)), "l"(global), "r"(bytes) : "memory");
@@ -432,8 +435,13 @@ __global__ void __launch_bounds__(32 * W, W <= 16 ? 32 / W : 1) ring_norm_kernel
 // the parts' sums.  The row read twice from shared memory with 1024 threads on an SM
 // took 41 instructions a value instead of 28 and 64 us, 1024 threads with one vector
 // each 73 us.  It wins for any number of rows from 64 vectors a row on, where norm_grad_kernel
-// would need a second warp a row (bf16, this and norm_grad_kernel: 1 x 7168 11 and 17 us, 64 x 7168 13 and
-// 19, 444 x 7168 17 and 38, 512 x 512 11 and 15; with 32 vectors 8192 x 256 24 both, 32768 x 256 62 and 36).
+// would need a second warp a row (bf16, this and norm_grad_kernel, with the parts' sums: 1 x 7168 6.5 and
+// 11.8 us, 64 x 7168 8.7 and 15.5, 444 x 7168 13 and 32, 512 x 512 6.2 and 9.9; with 32 vectors 8192 x 256
+// 18 and 21, 32768 x 256 57 and 32).
+// Rows of more than 1024 vectors take 1024 threads, whose 64 registers do not hold gains, running sums and the
+// row of the widest: bf16 kernels of more than 8192 columns spill 340 to 468 bytes a thread here and in
+// norm_grad_kernel, fp32 ones 296 to 404 in norm_grad_kernel; with the parts' sums 4096 x 9000 bf16 142 us,
+// 4096 x 16384 bf16 157 (2.6 TB/s), fp32 238 (3.4 TB/s).
 template <typename T, int W, bool LAYER>
 __global__ void __launch_bounds__(32 * W, W <= 16 ? 16 / W : 1) ring_norm_grad_kernel(const NormGradArgs a) {
   using R = Row<T, W, true>;
