@@ -1,6 +1,10 @@
 """Byte and FLOP counts bench.py divides by (host logic, CPU): the backward's
 bytes at the DeepSeek-V3 shape counted by hand, and the writes of the
 write-aware roofline."""
+import hashlib
+import json
+import os
+
 import numpy as np
 
 import bench
@@ -51,3 +55,16 @@ def test_e4m3_bytes_count_codes_and_row_scales():
     kept = np.full(w.E_r, 128)
     _, nbytes = bench.gateup_work(w, kept)
     assert nbytes == 257 * 2 * (7168 * 2048 + 4 * 2048) + 4096 * 7168 * 2
+
+
+def test_traffic_counters_are_of_the_current_gemm_source():
+    """bench.py reports DRAM traffic only from counters of the very source that it runs."""
+    root = os.path.dirname(os.path.abspath(bench.__file__))
+    with open(os.path.join(root, "profiles", "traffic.json")) as f:
+        doc = json.load(f)
+    with open(os.path.join(root, doc["source"]), "rb") as f:
+        assert hashlib.sha256(f.read()).hexdigest() == doc["source_sha256"]
+    for rec, bytes_of in (("ffn_gate_up", "impl_bytes"), ("ffn_down", "roofline_bytes")):
+        r = doc[rec]
+        ratio = r.get("ratio", r["ratio_to_roofline_bytes"])
+        assert abs(r["dram_bytes"] / r[bytes_of] - ratio) < 1e-4
