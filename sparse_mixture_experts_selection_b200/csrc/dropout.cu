@@ -3,8 +3,8 @@
 // u_i = word / 2^32 of Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel
 // random numbers: as easy as 1, 2, 3", 2011): block i / 4 of the counter,
 // word i % 4.  The mask is drawn again in the backward and never stored, so a
-// pass moves x, res and out and nothing else: 4096 x 7168 bf16 with a residual 32 us
-// (5.5 TB/s; torch's add of that size 28.8 us), 8191 x 2048 fp32 without 22.5 us
+// pass moves x, res and out and nothing else: 4096 x 7168 bf16 with a residual 32 to
+// 34 us (5.2 to 5.5 TB/s; torch's add of that size 28.8 us), 8191 x 2048 fp32 without 22.5 us
 // (6.0 TB/s).  2-byte values are bound by the instructions of the draw as much as by
 // memory, hence one block for four values and the keys made once.
 #include <cmath>
